@@ -58,7 +58,8 @@ enum {
   HSTU_SLA_ERR_CUDA = -3,         /* a CUDA runtime call failed */
   HSTU_SLA_ERR_BAD_INPUT = -4,    /* device-side check of offsets/targets failed */
   HSTU_SLA_ERR_WORKSPACE = -5,    /* workspace missing, too small or misaligned */
-  HSTU_SLA_ERR_TIMEOUT = -6       /* a bounded device-side wait gave up */
+  HSTU_SLA_ERR_TIMEOUT = -6,      /* a bounded device-side wait gave up */
+  HSTU_SLA_ERR_NO_PAGES = -7      /* hstu_cache.h: the free pages do not suffice */
 };
 
 /* Forward problem.  All integer fields are host values. */

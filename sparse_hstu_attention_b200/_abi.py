@@ -1,4 +1,4 @@
-"""ctypes view of include/hstu_sla.h (argument marshalling only)."""
+"""ctypes view of the headers under include/ (argument marshalling only)."""
 from __future__ import annotations
 
 import ctypes
@@ -9,7 +9,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libhstu_sla.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "hstu_sla.h")
 INCLUDE_DIR = os.path.join(os.path.dirname(PKG), "include")
-HEADERS = [HEADER, os.path.join(INCLUDE_DIR, "hstu_stu.h")]
+HEADERS = [HEADER, os.path.join(INCLUDE_DIR, "hstu_stu.h"),
+           os.path.join(INCLUDE_DIR, "hstu_cache.h")]
 
 OK = 0
 ERR_INVALID_ARG = -1
@@ -18,6 +19,7 @@ ERR_CUDA = -3
 ERR_BAD_INPUT = -4
 ERR_WORKSPACE = -5
 ERR_TIMEOUT = -6
+ERR_NO_PAGES = -7
 
 WS_FWD = 0
 WS_BWD = 1
@@ -106,6 +108,40 @@ class GemmParams(ctypes.Structure):
     ]
 
 
+class CacheTablesC(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("status", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+    ]
+
+
+class CacheRows(ctypes.Structure):
+    _fields_ = [
+        ("H", ctypes.c_int32), ("d", ctypes.c_int32), ("T", ctypes.c_int64),
+        ("slots", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_row_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64),
+    ]
+
+
+class CacheAttendParams(ctypes.Structure):
+    _fields_ = [
+        ("H", ctypes.c_int32), ("d", ctypes.c_int32), ("total_tokens", ctypes.c_int64),
+        ("max_new", ctypes.c_int32),
+        ("seq_offsets", ctypes.c_void_p), ("num_targets", ctypes.c_void_p),
+        ("contextual_len", ctypes.c_int32), ("K1", ctypes.c_int32), ("K2", ctypes.c_int32),
+        ("alpha", ctypes.c_float), ("N", ctypes.c_float),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+        ("v_row_stride", ctypes.c_int64),
+        ("pages", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_row_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -174,12 +210,27 @@ def load():
     lib.hstu_gemm.restype = ctypes.c_int
     lib.hstu_quant_weight_e4m3.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp]
     lib.hstu_quant_weight_e4m3.restype = ctypes.c_int
+    tab = ctypes.POINTER(CacheTablesC)
+    lib.hstu_cache_plan_workspace_bytes.argtypes = [i32]
+    lib.hstu_cache_plan_workspace_bytes.restype = sz
+    lib.hstu_cache_plan.argtypes = [tab, vp, vp, vp, i64, vp, vp, sz, vp]
+    lib.hstu_cache_plan.restype = ctypes.c_int
+    lib.hstu_cache_slot_map.argtypes = [tab, vp, i64, vp, vp]
+    lib.hstu_cache_slot_map.restype = ctypes.c_int
+    lib.hstu_cache_append.argtypes = [tab, ctypes.POINTER(CacheRows), vp]
+    lib.hstu_cache_append.restype = ctypes.c_int
+    lib.hstu_cache_read.argtypes = [tab, ctypes.POINTER(CacheRows), vp]
+    lib.hstu_cache_read.restype = ctypes.c_int
+    lib.hstu_cache_attend.argtypes = [tab, ctypes.POINTER(CacheAttendParams), vp]
+    lib.hstu_cache_attend.restype = ctypes.c_int
+    lib.hstu_cache_get_error.argtypes = [tab, vp]
+    lib.hstu_cache_get_error.restype = ctypes.c_int
     _lib = lib
     return lib
 
 
 def declared_functions():
-    """Names of the functions include/hstu_sla.h and include/hstu_stu.h declare."""
+    """Names of the functions the headers under include/ declare."""
     names = set()
     for h in HEADERS:
         text = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)

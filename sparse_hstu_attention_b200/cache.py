@@ -1,0 +1,314 @@
+"""Paged 4-bit history cache for serving (include/hstu_cache.h).
+
+Argument marshalling only, as in the package's other bindings: every step runs
+in the library's CUDA kernels.  A serving loop keeps the users' histories
+cached and brings only new rows, history events and candidates:
+
+    tables = cache.allocate_tables(B, max_pages, num_pages, page_size=64, device="cuda")
+    pages = [cache.allocate_pages(num_pages, H, d, 64, "cuda") for _ in layers]
+    ...
+    slots = cache.plan(tables, seq_offsets, num_targets, total_tokens=T)   # once a step
+    for each layer:
+        cache.append(k, v, slots, pages[l], tables)
+        out = cache.attend(q, k, v, seq_offsets, num_targets, pages[l], tables,
+                           contextual_len=32, K1=1024, K2=128, alpha=128 ** -0.5, N=16384.0)
+    cache.get_error(tables)   # when the program synchronises anyway
+
+Row b of the tables is a user slot; a step's batch has B sequences, one per
+slot, of any number of rows (none for a slot with nothing new).  There is no
+gradient: the outputs are new tensors outside autograd.
+
+Calls run on the tensors' own device, on its current stream unless `stream` is
+given, and allocate only their outputs (and plan its scratch).  They can be
+captured into a CUDA graph and replayed with other lengths, counts and offsets
+in the same tensors: nothing about them is read on the host.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import SLAError, _abi
+
+__all__ = ["CacheTables", "allocate_tables", "allocate_pages", "plan", "slot_map", "append",
+           "read", "attend", "get_error"]
+
+_HEADER = 64  # int32 words before the lengths: word 0 the status, word 16 the free count
+
+
+def _pad(n: int) -> int:
+    return (n + 63) // 64 * 64
+
+
+class CacheTables:
+    """Lengths, free pages and block table of B user slots, in one contiguous
+    CUDA int32 buffer (`buf.clone()` copies the whole state): a header of 64
+    words (word 0 the status, word 16 the number of free pages), lengths [B],
+    free_pages [num_pages], block_table [B, max_pages], each part starting at a
+    multiple of 64 words."""
+
+    __slots__ = ("buf", "B", "max_pages", "num_pages", "page_size", "_c")
+
+    def __init__(self, buf: torch.Tensor, B: int, max_pages: int, num_pages: int,
+                 page_size: int):
+        if buf.dtype != torch.int32 or not buf.is_cuda or not buf.is_contiguous():
+            raise TypeError("buf must be a contiguous CUDA int32 tensor")
+        if B < 1 or max_pages < 1 or num_pages < 1:
+            raise ValueError("B, max_pages and num_pages must be at least 1")
+        if buf.numel() < self.words(B, max_pages, num_pages):
+            raise ValueError(f"buf has {buf.numel()} words, needs "
+                             f"{self.words(B, max_pages, num_pages)}")
+        self.buf, self.B, self.max_pages = buf, int(B), int(max_pages)
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        p = buf.data_ptr()
+        free = p + 4 * (_HEADER + _pad(self.B))
+        self._c = _abi.CacheTablesC(self.B, self.max_pages, self.num_pages, self.page_size, p,
+                                    p + 64, p + 4 * _HEADER, free, free + 4 * _pad(self.num_pages))
+
+    @staticmethod
+    def words(B: int, max_pages: int, num_pages: int) -> int:
+        return _HEADER + _pad(B) + _pad(num_pages) + B * max_pages
+
+    @property
+    def status(self) -> torch.Tensor:
+        return self.buf[0:1]
+
+    @property
+    def free_count(self) -> torch.Tensor:
+        return self.buf[16:17]
+
+    @property
+    def lengths(self) -> torch.Tensor:
+        return self.buf[_HEADER:_HEADER + self.B]
+
+    @property
+    def free_pages(self) -> torch.Tensor:
+        at = _HEADER + _pad(self.B)
+        return self.buf[at:at + self.num_pages]
+
+    @property
+    def block_table(self) -> torch.Tensor:
+        at = _HEADER + _pad(self.B) + _pad(self.num_pages)
+        return self.buf[at:at + self.B * self.max_pages].view(self.B, self.max_pages)
+
+
+def allocate_tables(B: int, max_pages: int, num_pages: int, *, page_size: int = 64,
+                    device="cuda") -> CacheTables:
+    """Tables of an empty cache: all lengths 0, all pages free (page 0 on top)."""
+    buf = torch.zeros(CacheTables.words(B, max_pages, num_pages), dtype=torch.int32,
+                      device=device)
+    t = CacheTables(buf, B, max_pages, num_pages, page_size)
+    t.free_count.fill_(num_pages)
+    t.free_pages.copy_(torch.arange(num_pages - 1, -1, -1, dtype=torch.int32))
+    return t
+
+
+def allocate_pages(num_pages: int, H: int, d: int, page_size: int = 64,
+                   device="cuda") -> torch.Tensor:
+    """One layer's pages: uint8 [num_pages, H, page_size * (d + 8)]; their
+    contents need not be initialised."""
+    return torch.empty((num_pages, H, page_size * (d + 8)), dtype=torch.uint8, device=device)
+
+
+class _On:
+    """The library calls launch on the current device: make it the tensors'."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, device: torch.device):
+        same = device.index is None or device.index == torch.cuda.current_device()
+        self.guard = None if same else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _check(code: int, where: str):
+    if code != _abi.OK:
+        raise SLAError(code, where)
+
+
+def _stream(stream, device) -> int:
+    return int((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+
+
+def _i32(t: Optional[torch.Tensor], n: int, name: str, device) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor on {device}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, T: int, H: int, d: int, device) -> int:
+    """Checks a bf16 [T, H, d] tensor; returns its row stride."""
+    if t.dtype != torch.bfloat16 or t.device != device:
+        raise TypeError(f"{name} must be a bfloat16 tensor on {device}")
+    if t.shape != (T, H, d):
+        raise ValueError(f"{name} must be [{T}, {H}, {d}], got {tuple(t.shape)}")
+    if T > 0 and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: heads and head_dim must be dense (stride (*, {d}, 1))")
+    return t.stride(0) if T > 1 else H * d
+
+
+def _pages(pages: torch.Tensor, tables: CacheTables):
+    """(H, d, page stride in bytes) of a pages tensor."""
+    if pages.dtype != torch.uint8 or pages.device != tables.buf.device or pages.dim() != 3:
+        raise TypeError("pages must be a uint8 tensor [num_pages, H, page_size * (d + 8)] on the "
+                        "tables' device")
+    P, H, n = pages.shape
+    ps = tables.page_size
+    d = n // ps - 8
+    if P != tables.num_pages or H < 1 or d < 1 or n != ps * (d + 8):
+        raise ValueError(f"pages must be [{tables.num_pages}, H, {ps} * (d + 8)], got "
+                         f"{tuple(pages.shape)}")
+    if pages.stride(2) != 1 or (H > 1 and pages.stride(1) != n):
+        raise ValueError("pages: the heads of a page must be dense")
+    return H, d, pages.stride(0) if P > 1 else H * n
+
+
+def plan(tables: CacheTables, seq_offsets: torch.Tensor, num_targets: Optional[torch.Tensor] = None,
+         *, total_tokens: int, release: Optional[torch.Tensor] = None,
+         slots: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+         stream=None) -> torch.Tensor:
+    """One step's pages, slots and lengths (include/hstu_cache.h,
+    hstu_cache_plan), written into `tables`; returns slots, int64
+    [total_tokens], -1 for candidates and for rows behind seq_offsets[B].
+    seq_offsets: int32 [B + 1]; num_targets: int32 [B], the trailing candidates
+    of each sequence; release: int32 [B], non-zero empties the slot first."""
+    dev = tables.buf.device
+    o = _i32(seq_offsets, tables.B + 1, "seq_offsets", dev)
+    nt = _i32(num_targets, tables.B, "num_targets", dev)
+    rel = _i32(release, tables.B, "release", dev)
+    slots = _slots_out(slots, total_tokens, dev)
+    lib = _abi.load()
+    need = lib.hstu_cache_plan_workspace_bytes(tables.B)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must have {need} bytes on {dev}")
+    with _On(dev):
+        _check(lib.hstu_cache_plan(tables._c, o, nt, rel, total_tokens, slots.data_ptr(),
+                                   workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(),
+                                   _stream(stream, dev)), "hstu_cache_plan")
+    return slots
+
+
+def _slots_out(slots, total_tokens, dev):
+    if slots is None:
+        return torch.empty(total_tokens, dtype=torch.int64, device=dev)
+    _slots(slots, dev)
+    if slots.numel() != total_tokens:
+        raise ValueError(f"slots must have {total_tokens} elements")
+    return slots
+
+
+def _slots(slots, dev):
+    if slots.dtype != torch.int64 or slots.device != dev or slots.dim() != 1 or \
+            not slots.is_contiguous():
+        raise TypeError(f"slots must be a contiguous int64 vector on {dev}")
+
+
+def slot_map(tables: CacheTables, seq_offsets: torch.Tensor, *, total_tokens: int,
+             slots: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Slots of the last seq_offsets[b + 1] - seq_offsets[b] cached tokens of
+    every sequence (e.g. to read whole histories back)."""
+    dev = tables.buf.device
+    o = _i32(seq_offsets, tables.B + 1, "seq_offsets", dev)
+    slots = _slots_out(slots, total_tokens, dev)
+    with _On(dev):
+        _check(_abi.load().hstu_cache_slot_map(tables._c, o, total_tokens, slots.data_ptr(),
+                                               _stream(stream, dev)), "hstu_cache_slot_map")
+    return slots
+
+
+def _row_call(k, v, slots, pages, tables, H, d, page_stride):
+    dev = tables.buf.device
+    T = slots.numel()
+    return _abi.CacheRows(H, d, T, slots.data_ptr(), pages.data_ptr(), page_stride, k.data_ptr(),
+                          v.data_ptr(), _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev))
+
+
+def append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pages: torch.Tensor,
+           tables: CacheTables, *, stream=None) -> None:
+    """Quantise the rows of k and v ([T, H, d] bf16) into `pages` at `slots`
+    (rows with a negative slot are skipped)."""
+    H, d, stride = _pages(pages, tables)
+    dev = tables.buf.device
+    _slots(slots, dev)
+    r = _row_call(k, v, slots, pages, tables, H, d, stride)
+    with _On(dev):
+        _check(_abi.load().hstu_cache_append(tables._c, r, _stream(stream, dev)),
+               "hstu_cache_append")
+
+
+def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
+         k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, stream=None):
+    """The rows that `slots` hold, as bf16 (k, v) [T, H, d]; zeros for a
+    negative slot."""
+    H, d, stride = _pages(pages, tables)
+    dev = tables.buf.device
+    _slots(slots, dev)
+    T = slots.numel()
+    if k is None:
+        k = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+    r = _row_call(k, v, slots, pages, tables, H, d, stride)
+    with _On(dev):
+        _check(_abi.load().hstu_cache_read(tables._c, r, _stream(stream, dev)),
+               "hstu_cache_read")
+    return k, v
+
+
+def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+           seq_offsets: torch.Tensor, num_targets: Optional[torch.Tensor], pages: torch.Tensor,
+           tables: CacheTables, *, contextual_len: int, K1: int, K2: int, alpha: float, N: float,
+           max_new: Optional[int] = None, out: Optional[torch.Tensor] = None,
+           stream=None) -> torch.Tensor:
+    """SLA HSTU attention of the step's rows over the cached histories; returns
+    out [T, H, d] bf16 (rows behind seq_offsets[B] are left as they were).  The
+    step's history rows are in the cache already (plan, append); a candidate
+    sees the history and, through its own row of k and v, itself.  k and v may
+    be None when num_targets is.  max_new: a bound on the rows of any sequence
+    (default: all of them); a tight one gives a step of few rows its kernel."""
+    H, d, stride = _pages(pages, tables)
+    dev = tables.buf.device
+    T = q.shape[0]
+    q_rs = _rows(q, "q", T, H, d, dev)
+    k_ptr = v_ptr = None
+    k_rs = v_rs = 0
+    if num_targets is not None:
+        if k is None or v is None:
+            raise ValueError("candidates (num_targets) need their rows of k and v")
+        k_rs, v_rs = _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev)
+        k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
+    if out is None:
+        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+    p = _abi.CacheAttendParams(
+        H, d, T, T if max_new is None else int(max_new),
+        _i32(seq_offsets, tables.B + 1, "seq_offsets", dev),
+        _i32(num_targets, tables.B, "num_targets", dev), int(contextual_len), int(K1), int(K2),
+        float(alpha), float(N), q.data_ptr(), k_ptr, v_ptr, q_rs, k_rs, v_rs, pages.data_ptr(),
+        stride, out.data_ptr(), _rows(out, "out", T, H, d, dev))
+    with _On(dev):
+        _check(_abi.load().hstu_cache_attend(tables._c, p, _stream(stream, dev)),
+               "hstu_cache_attend")
+    return out
+
+
+def get_error(tables: CacheTables, stream=None) -> int:
+    """Synchronise and return the tables' status (0 = no error)."""
+    dev = tables.buf.device
+    with _On(dev):
+        return int(_abi.load().hstu_cache_get_error(tables._c, _stream(stream, dev)))

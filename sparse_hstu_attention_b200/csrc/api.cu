@@ -10,8 +10,8 @@ using namespace hstu;
 namespace {
 
 // 101: hstu_sla_fwd_params.candidates_only; 102: FP8 forward; 103: grouped calls;
-// 104: relative attention bias
-constexpr int kAbiVersion = 105;
+// 104: relative attention bias; 106: paged history cache (hstu_cache.h)
+constexpr int kAbiVersion = 106;
 static_assert(HSTU_SLA_MAX_GROUPS == kMaxGroups, "one grouped launch holds every group");
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -354,6 +354,7 @@ const char* hstu_sla_strerror(int code) {
     case HSTU_SLA_ERR_BAD_INPUT: return "invalid seq_offsets / num_targets detected on the device";
     case HSTU_SLA_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
     case HSTU_SLA_ERR_TIMEOUT: return "a bounded device-side wait timed out";
+    case HSTU_SLA_ERR_NO_PAGES: return "the free pages do not suffice for the new rows";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,476 @@
+"""The paged 4-bit history cache on the GPU against plain 64-bit forms
+(tests/cache_ref.py): stored bytes and read rows bit for bit, plans as whole
+numbers, attention within the bound derived in cache_ref.attend."""
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as ref
+from sparse_hstu_attention_b200 import _abi, cache
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def dev32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device=DEV)
+
+
+def offs_of(rows):
+    return dev32(np.concatenate([[0], np.cumsum(rows)]))
+
+
+def silu_rows(T, H, d, seed, strided=True):
+    """q, k, v [T, H, d] bf16 on the CPU, as column blocks of one projection."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.nn.functional.silu(torch.randn((max(T, 1), 4 * H * d), generator=g)).bfloat16()[:T]
+    q, k, v = (x[:, i * H * d:(i + 1) * H * d].reshape(T, H, d) for i in (2, 3, 1))
+    return q, k, v
+
+
+def on_gpu(x, wide):
+    """x on the GPU; `wide`: as a view into rows 4 times as long."""
+    T, H, d = x.shape
+    if not wide:
+        return x.to(DEV)
+    buf = torch.full((T, 4 * H * d), float("nan"), dtype=x.dtype, device=DEV)
+    out = buf[:, H * d:2 * H * d].unflatten(1, (H, d))
+    out.copy_(x)
+    return out
+
+
+def tables_of(lengths, ps, seed, spare=3, most=None):
+    """Tables whose sequence b holds lengths[b] tokens in pages drawn at random;
+    the host copy beside the GPU's."""
+    g = np.random.default_rng(seed)
+    used = [-(-n // ps) for n in lengths]
+    M = max(1, most or max(used))
+    P = max(1, sum(used) + spare)
+    perm = g.permutation(P)
+    bt = g.integers(0, 2 ** 31 - 1, size=(len(lengths), M))  # unused entries are garbage
+    at = P - sum(used)
+    free = perm[:at]
+    for b, n in enumerate(used):
+        bt[b, :n] = perm[at:at + n]
+        at += n
+    t = cache.allocate_tables(len(lengths), M, P, page_size=ps, device=DEV)
+    t.lengths.copy_(dev32(lengths))
+    t.block_table.copy_(torch.from_numpy(bt.astype(np.int32)))
+    t.free_pages[:len(free)] = torch.from_numpy(free.astype(np.int32)).to(DEV)
+    t.free_count.fill_(len(free))
+    return t, ref.Tables(lengths, bt, free, P, ps)
+
+
+# ------------------------------------------------------------ append and read
+@pytest.mark.parametrize("H,d,ps,T", [(1, 32, 16, 1), (2, 64, 32, 7), (3, 128, 64, 130),
+                                      (4, 128, 16, 333), (2, 32, 64, 4100), (1, 64, 16, 17),
+                                      (40, 128, 64, 700)])
+@pytest.mark.parametrize("order", ["runs", "mixed"])
+def test_append_and_read(H, d, ps, T, order):
+    """Every byte of the pages as the plain form has it, the untouched ones as
+    they were; rows read back are m + s code in bf16."""
+    g = np.random.default_rng(T)
+    P = T // ps + 4
+    if order == "runs":  # sequences of consecutive slots, starting anywhere
+        slots, s = [], int(g.integers(0, ps))
+        while len(slots) < T and s < P * ps:
+            n = int(g.integers(1, 200))
+            slots += list(range(s, min(s + n, P * ps)))
+            s += n + int(g.integers(0, 3))
+        slots = slots[:T] + [-1] * max(0, T - len(slots))
+    else:
+        slots = g.permutation(P * ps)[:T].tolist()
+    slots = torch.tensor(slots)
+    if T > 5:
+        slots[g.integers(0, T, 3)] = -1
+    _, k, v = silu_rows(T, H, d, T)
+    k[0] = 0.5           # no range: step 0
+    if T > 5:
+        k[3, 0, 1], v[4, 0, 2], v[5, 0, 0] = float("nan"), float("inf"), -float("inf")
+        v[1], k[2] = v[1] * 1e-39, k[2] * 1e30   # steps that vanish, and large ones
+        k[1, 0, 0], k[1, 0, 1] = 3e38, -3e38     # a range beyond fp32
+    pages = torch.from_numpy(g.integers(0, 256, size=(P, H, ps * (d + 8)), dtype=np.uint8))
+    want = ref.pack(pages.clone(), ps, slots, k, v)
+    t = cache.allocate_tables(1, 1, P, page_size=ps, device=DEV)
+    got = pages.to(DEV)
+    cache.append(on_gpu(k, True), on_gpu(v, T % 2 == 0), slots.to(DEV), got, t)
+    kept = [s for s in slots.tolist() if s >= 0]
+    # a NaN pair may have any NaN's bits: compare it as NaN, everything else as bytes
+    K0, V0 = ref.unpack(want, ps, d)
+    K1, V1 = ref.unpack(got, ps, d)
+    for x, y in ((K0, K1), (V0, V1)):
+        x, y = x.reshape(-1, H, d)[kept], y.reshape(-1, H, d)[kept]
+        assert torch.equal(x.isnan(), y.isnan())
+        assert torch.equal(x.nan_to_num(), y.nan_to_num())
+    odd = (got.cpu() != want).sum().item()
+    assert odd <= 6 * 4  # at most the bytes of the few NaN pairs
+    rk, rv = cache.read(slots.to(DEV), got, t)
+    for x, y in ((K0, rk), (V0, rv)):
+        x = x.reshape(-1, H, d)[slots.clamp(min=0)]
+        x[slots < 0] = 0
+        y = y.cpu().double()
+        assert torch.equal(x.isnan(), y.isnan())
+        assert torch.equal(x.float().bfloat16().double().nan_to_num(), y.nan_to_num())
+    assert cache.get_error(t) == 0
+
+
+def test_slots_beyond_the_pages_are_reported_and_write_nothing():
+    t = cache.allocate_tables(1, 1, 3, page_size=16, device=DEV)
+    pages = torch.full((3, 1, 16 * 40), 77, dtype=torch.uint8, device=DEV)
+    _, k, v = (x.to(DEV) for x in silu_rows(2, 1, 32, 0))
+    cache.append(k, v, torch.tensor([48, 1 << 40], device=DEV), pages, t)
+    assert cache.get_error(t) == _abi.ERR_BAD_INPUT
+    assert bool((pages == 77).all())
+    cache.append(k, v, torch.tensor([0, 1], device=DEV), pages, t)  # still set: nothing is done
+    assert bool((pages == 77).all())
+
+
+# ---------------------------------------------------------------------- plan
+def check_plan(t, host, rows, cand, release, pad=0):
+    T = int(sum(rows))
+    slots = cache.plan(t, offs_of(rows), dev32(cand) if any(cand) else None, total_tokens=T + pad,
+                       release=dev32(release) if any(release) else None)
+    want = host.plan(rows, cand, release, T + pad)
+    assert cache.get_error(t) == 0
+    assert slots.tolist() == want
+    assert t.lengths.tolist() == host.lengths
+    assert int(t.free_count) == host.count
+    assert t.free_pages.tolist()[:host.count] == host.stack[:host.count]
+    assert t.block_table.tolist() == host.bt
+    return slots
+
+
+@pytest.mark.parametrize("B,ps,most,seed", [(1, 64, 1, 0), (5, 16, 40, 1), (64, 32, 3, 2),
+                                            (1500, 16, 20, 3), (3, 64, 9000, 4),
+                                            (2500, 32, 60, 5)])
+def test_plan_matches_a_walk(B, ps, most, seed):
+    """Several steps in a row: appends, candidates, rows behind the last
+    sequence, slots that change hands (one block up to 8192 rows, a grid above)."""
+    g = np.random.default_rng(seed)
+    lengths = g.integers(0, 3 * ps, size=B).tolist()
+    M = -(-(3 * ps + 3 * most) // ps) + 1
+    t, host = tables_of(lengths, ps, seed, spare=B * (2 + 3 * most // ps), most=M)
+    for step in range(3):
+        fresh = np.where(g.random(B) < 0.7, g.integers(0, most, size=B, endpoint=True), 0)
+        cand = np.where(g.random(B) < 0.5, g.integers(0, 5, size=B), 0) * (step > 0)
+        release = (g.random(B) < 0.3) * (step == 2)
+        check_plan(t, host, (fresh + cand).tolist(), cand.tolist(), release.astype(int).tolist(),
+                   pad=7 * step)
+
+
+def test_plan_without_pages_changes_nothing():
+    for total in (0, 20000):  # one block, and the grid
+        t, _ = tables_of([10, 20, 30], 16, 1, spare=2, most=4000)
+        before = t.buf.clone()
+        rows = [20, 20, 20 + total]
+        slots = cache.plan(t, offs_of(rows), total_tokens=sum(rows))
+        assert cache.get_error(t) == _abi.ERR_NO_PAGES
+        assert bool((slots == -1).all())
+        assert torch.equal(t.buf[16:], before[16:])
+        # the other calls do nothing until a plan succeeds
+        pages = torch.full((t.num_pages, 1, 16 * 40), 5, dtype=torch.uint8, device=DEV)
+        out = torch.full((60 + total, 1, 32), 7.0, dtype=torch.bfloat16, device=DEV)
+        q, k, v = (x.to(DEV) for x in silu_rows(60 + total, 1, 32, 0))
+        cache.append(k, v, torch.arange(60 + total, device=DEV) % 40, pages, t)
+        assert bool((pages == 5).all())
+        slots = cache.plan(t, offs_of([1, 0, 0]), total_tokens=1)
+        assert cache.get_error(t) == 0 and int(slots[0]) >= 0
+
+
+@pytest.mark.parametrize("what", ["down", "past", "first", "targets", "long", "length", "count"])
+def test_plan_refuses_bad_inputs(what):
+    t, _ = tables_of([10, 20], 16, 1, spare=9, most=4)
+    offs, nt = [0, 3, 6], [0, 1]
+    if what == "down":
+        offs = [0, 5, 3]
+    if what == "past":
+        offs = [0, 3, 9]
+    if what == "first":
+        offs = [1, 3, 6]
+    if what == "targets":
+        nt = [0, 4]
+    if what == "long":
+        offs = [0, 55, 55]
+    if what == "length":
+        t.lengths[1] = -4
+    if what == "count":
+        t.free_count.fill_(t.num_pages + 1)
+    before = t.buf.clone()
+    T = 55 if what == "long" else 6
+    nt = [0, 0] if what == "long" else nt
+    slots = cache.plan(t, dev32(offs), dev32(nt), total_tokens=T)
+    assert cache.get_error(t) == _abi.ERR_BAD_INPUT
+    assert bool((slots == -1).all()) and torch.equal(t.buf[16:], before[16:])
+
+
+def test_slot_map_gives_the_last_tokens():
+    lengths = [40, 0, 7, 130]
+    t, host = tables_of(lengths, 32, 3)
+    rows = [33, 0, 7, 64]
+    slots = cache.slot_map(t, offs_of(rows), total_tokens=sum(rows) + 3).tolist()
+    want = []
+    for b, n in enumerate(rows):
+        want += [host.bt[b][p // 32] * 32 + p % 32 for p in range(lengths[b] - n, lengths[b])]
+    assert slots == want + [-1] * 3 and cache.get_error(t) == 0
+    slots = cache.slot_map(t, offs_of([41, 0, 0, 1]), total_tokens=42).tolist()
+    assert slots[:41] == [-1] * 41 and cache.get_error(t) == _abi.ERR_BAD_INPUT
+
+
+# -------------------------------------------------------------------- attend
+def filled(lengths, H, d, ps, seed, garbage=True):
+    """Tables and pages holding random histories; per sequence the codes and
+    pairs, token by token.  Unused bytes are garbage (NaN pairs among them)."""
+    t, host = tables_of(lengths, ps, seed)
+    g = torch.Generator().manual_seed(seed)
+    pages = torch.full((t.num_pages, H, ps * (d + 8)), 255 if garbage else 0, dtype=torch.uint8)
+    tokens = []
+    for b, n in enumerate(lengths):
+        _, k, v = silu_rows(n, H, d, seed * 100 + b)
+        slots = torch.tensor([host.bt[b][p // ps] * ps + p % ps for p in range(n)],
+                             dtype=torch.int64)
+        if n:
+            pages = ref.pack(pages, ps, slots, k, v)
+        tokens.append(tuple((c.double(), s, m) for c, s, m in (ref.quantise(k), ref.quantise(v)))
+                      if n else ((torch.zeros(0, H, d).double(), torch.zeros(0, H).double(),
+                                  torch.zeros(0, H).double()),) * 2)
+    return t, pages.to(DEV), tokens
+
+
+def run_attend(t, pages, tokens, lengths, rows, cand, H, d, seed, *, K1, K2, ctx, max_new=None,
+               pad=0, wide=True, edit=None):
+    T = int(sum(rows))
+    q, k, v = silu_rows(T, H, d, seed + 1)
+    if edit:
+        edit(q, k, v)
+    alpha, N = d ** -0.5, 100.0
+    out = torch.full((T + pad, H, d), 3.0, dtype=torch.bfloat16, device=DEV)
+    more = torch.full((pad, H, d), float("nan")).bfloat16()
+    qg, kg, vg = (on_gpu(torch.cat([x, more]), wide) for x in (q, k, v))
+    has = any(cand)
+    cache.attend(qg, kg if has else None, vg if has else None, offs_of(rows),
+                 dev32(cand) if has else None, pages, t, contextual_len=ctx, K1=K1, K2=K2,
+                 alpha=alpha, N=N, max_new=max_new, out=out)
+    assert cache.get_error(t) == 0
+    assert bool((out[T:] == 3.0).all())
+    want, tol = ref.attend(q, k, v, rows, cand, lengths, tokens, K1=K1, K2e=max(K2, ctx),
+                           alpha=alpha, N=N)
+    return out[:T].cpu().double(), want, tol
+
+
+def check(got, want, tol):
+    bad = ~((got - want).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), float(((got - want).abs() / tol).max()))
+
+
+FEW = [([300], [1], [0]), ([0, 5, 64, 65, 700], [3, 1, 1, 2, 0], [3, 0, 1, 0, 0]),
+       ([128, 1, 17], [16, 1, 16], [4, 0, 16]), ([2100, 900], [1, 1], [0, 0])]
+MANY = [([200], [17], [0]), ([500, 3, 0], [130, 40, 33], [2, 40, 33]),
+        ([300, 129, 128], [300, 129, 1], [0, 0, 0]), ([1000, 260], [150, 300], [150, 270])]
+
+
+HEADS = [(2, 32, 16), (1, 64, 32), (3, 128, 64), (1, 128, 16), (2, 64, 64), (2, 32, 32)]
+WINDOWS = [(1 << 20, 0, 0), (100, 20, 33), (0, 0, 0), (1, 0, 0), (0, 70, 0)]
+
+
+@pytest.mark.parametrize("case,heads,window",
+                         [(c, h, w) for c in range(8) for h in HEADS for w in WINDOWS
+                          if c < 4 or h not in HEADS[4:] or w == WINDOWS[1]])
+def test_attend(case, heads, window):
+    (H, d, ps), (K1, K2, ctx) = heads, window
+    lengths, rows, cand = (FEW + MANY)[case]
+    t, pages, tokens = filled(lengths, H, d, ps, case + 1)
+    got, want, tol = run_attend(t, pages, tokens, lengths, rows, cand, H, d, case, K1=K1, K2=K2,
+                                ctx=ctx, max_new=max(rows), pad=case % 3, wide=case % 2 == 0)
+    check(got, want, tol)
+    if K1 == K2 == ctx == 0:  # history rows see nothing
+        at = 0
+        for n, c in zip(rows, cand):
+            assert bool((got[at:at + n - c] == 0).all())
+            at += n
+
+
+def test_what_is_masked_does_not_reach_a_row():
+    """NaN and infinities in tokens outside the window, in other candidates'
+    rows and behind the length change nothing."""
+    H, d, ps = 2, 64, 32
+    lengths, K1 = [200, 300], 50
+    for rows, cand in (([3, 4], [2, 4]), ([40, 30], [30, 25])):
+        t, pages, tokens = filled(lengths, H, d, ps, 9)
+        q, k, v = silu_rows(sum(rows), H, d, 10)
+        args = dict(contextual_len=0, K1=K1, K2=0, alpha=0.1, N=10.0, max_new=max(rows))
+        offs, nts = offs_of(rows), dev32(cand)
+        qg, kg, vg = q.to(DEV), k.to(DEV), v.to(DEV)
+        clean = cache.attend(qg, kg, vg, offs, nts, pages, t, **args)
+        # tokens below every row's window become NaN, one candidate's row too
+        slots = []
+        for b, L in enumerate(lengths):
+            low = L - (rows[b] - cand[b]) - K1
+            slots += [int(t.block_table[b, p // ps]) * ps + p % ps for p in range(max(0, low))]
+        bad = torch.full((len(slots), H, d), float("nan")).bfloat16().to(DEV)
+        cache.append(bad, bad, torch.tensor(slots, device=DEV), pages, t)
+        last = sum(rows) - 1
+        kg[last], vg[last] = float("nan"), float("inf")
+        got = cache.attend(qg, kg, vg, offs, nts, pages, t, **args)
+        assert torch.equal(got[:last], clean[:last])
+        assert bool(got[last].isnan().all())
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_pages_far_apart(rows):
+    """Page offsets beyond 32 bits."""
+    H, d, ps = 1, 128, 64
+    lengths = [150, 90]
+    t, pages, tokens = filled(lengths, H, d, ps, 4)
+    stride = (1 << 30) + 256
+    buf = torch.empty(stride * (t.num_pages - 1) + pages[0].numel(), dtype=torch.uint8,
+                      device=DEV)
+    far = torch.as_strided(buf, pages.shape, (stride, ps * (d + 8), 1))
+    far.copy_(pages)
+    got, want, tol = run_attend(t, far, tokens, lengths, [rows, rows], [0, 0], H, d, 1, K1=1 << 20,
+                                K2=0, ctx=0, max_new=rows)
+    check(got, want, tol)
+    slots = cache.slot_map(t, offs_of([5, 5]), total_tokens=10)
+    for x, y in zip(cache.read(slots, far, t), cache.read(slots, pages, t)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("what", ["page", "length", "offsets", "targets", "rows"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_attend_reports_bad_inputs(what, n):
+    H, d, ps = 2, 32, 16
+    t, pages, _ = filled([60, 80], H, d, ps, 5, garbage=False)
+    q, k, v = (x.to(DEV) for x in silu_rows(2 * n, H, d, 0))
+    offs, nts, most = [0, n, 2 * n], [0, 1], n
+    if what == "page":
+        t.block_table[1, 2] = t.num_pages
+    if what == "length":
+        t.lengths[0] = 1 << 20
+    if what == "offsets":
+        offs = [0, n, 2 * n + 1]
+    if what == "targets":
+        nts = [0, n + 1]
+    if what == "rows":
+        offs, most = [0, 0, 2 * n], n
+    out = cache.attend(q, k, v, dev32(offs), dev32(nts), pages, t, contextual_len=0, K1=1 << 20,
+                       K2=0, alpha=0.1, N=10.0, max_new=most)
+    assert out.shape == q.shape and cache.get_error(t) == _abi.ERR_BAD_INPUT
+
+
+# ------------------------------------------------------------------ together
+def test_a_serving_run():
+    """Steps as a server makes them: histories come in whole, users bring single
+    events and candidates, one slot changes hands; every output against the
+    plain form over what was stored."""
+    H, d, ps, B, K1, K2, ctx = 2, 64, 32, 4, 60, 20, 4
+    t = cache.allocate_tables(B, 12, 40, page_size=ps, device=DEV)
+    pages = [cache.allocate_pages(40, H, d, ps, DEV) for _ in range(2)]
+    kept = [[None] * B for _ in pages]
+    lengths = [0] * B
+    steps = [([150, 70, 0, 33], [0, 0, 0, 0], [0] * 4), ([1, 1, 0, 1], [0, 0, 0, 0], [0] * 4),
+             ([20, 9, 6, 0], [20, 8, 6, 0], [0] * 4), ([90, 0, 40, 2], [0, 0, 10, 1], [1, 0, 0, 0]),
+             ([1, 2, 1, 18], [0, 1, 0, 18], [0] * 4)]
+    for n, (rows, cand, release) in enumerate(steps):
+        T = sum(rows)
+        offs, nts = offs_of(rows), dev32(cand)
+        slots = cache.plan(t, offs, nts, total_tokens=T,
+                           release=dev32(release) if any(release) else None)
+        lengths = [(0 if g else x) + r - c for x, r, c, g in zip(lengths, rows, cand, release)]
+        for layer, pg in enumerate(pages):
+            q, k, v = silu_rows(T, H, d, 50 * n + layer)
+            at = 0
+            for b in range(B):
+                new = tuple(ref.quantise(x[at:at + rows[b] - cand[b]]) for x in (k, v))
+                old = kept[layer][b]
+                if old is None or release[b]:
+                    kept[layer][b] = tuple(tuple(y.double() for y in x) for x in new)
+                else:
+                    kept[layer][b] = tuple(tuple(torch.cat([y, z.double()]) for y, z in zip(o, x))
+                                           for o, x in zip(old, new))
+                at += rows[b]
+            qg, kg, vg = (on_gpu(x, True) for x in (q, k, v))
+            cache.append(kg, vg, slots, pg, t)
+            out = cache.attend(qg, kg, vg, offs, nts, pg, t, contextual_len=ctx, K1=K1, K2=K2,
+                               alpha=d ** -0.5, N=64.0, max_new=max(rows))
+            want, tol = ref.attend(q, k, v, rows, cand, lengths, kept[layer], K1=K1,
+                                   K2e=max(K2, ctx), alpha=d ** -0.5, N=64.0)
+            check(out.cpu().double(), want, tol)
+        assert t.lengths.tolist() == lengths and cache.get_error(t) == 0
+
+
+def test_a_captured_step_replays_with_other_lengths():
+    """One graph of plan, append and attend on a side stream, replayed with new
+    offsets, targets and rows in the same tensors, gives what plain calls give."""
+    H, d, ps, B, T = 2, 32, 16, 3, 24
+    s = torch.cuda.Stream()
+    bufs = [torch.zeros((T, H, d), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    offs, nts = dev32([0, 1, 2, 3]), dev32([0, 0, 0])
+    ws = torch.empty(4096, dtype=torch.uint8, device=DEV)
+    slots = torch.empty(T, dtype=torch.int64, device=DEV)
+    out = torch.zeros((T, H, d), dtype=torch.bfloat16, device=DEV)
+
+    def fresh():
+        return (cache.allocate_tables(B, 8, 20, page_size=ps, device=DEV),
+                torch.zeros((20, H, ps * (d + 8)), dtype=torch.uint8, device=DEV))
+
+    def step(t, pages, slots, out, ws):
+        cache.plan(t, offs, nts, total_tokens=T, slots=slots, workspace=ws)
+        cache.append(bufs[1], bufs[2], slots, pages, t)
+        cache.attend(*bufs, offs, nts, pages, t, contextual_len=2, K1=20, K2=4, alpha=0.2, N=8.0,
+                     out=out)
+
+    t1, p1 = fresh()
+    t2, p2 = fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        graph.capture_begin()
+        step(t1, p1, slots, out, ws)
+        graph.capture_end()
+    torch.cuda.synchronize()
+    for n, (rows, cand) in enumerate([([20, 1, 3], [0, 0, 0]), ([1, 9, 1], [0, 8, 0]),
+                                      ([0, 1, 23], [0, 1, 20])]):
+        offs.copy_(offs_of(rows))
+        nts.copy_(dev32(cand))
+        for x, y in zip(bufs, silu_rows(T, H, d, n)):
+            x.copy_(y)
+        out.fill_(9.0)
+        other = torch.full_like(out, 9.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+        s.synchronize()
+        sl = torch.empty_like(slots)
+        step(t2, p2, sl, other, torch.empty_like(ws))
+        torch.cuda.synchronize()
+        assert torch.equal(sl, slots) and torch.equal(t1.buf, t2.buf) and torch.equal(p1, p2)
+        assert torch.equal(out, other) and cache.get_error(t1) == 0
+
+
+def test_python_refusals():
+    t, pages, _ = filled([20], 2, 32, 16, 1)
+    q, k, v = (x.to(DEV) for x in silu_rows(2, 2, 32, 0))
+    offs = offs_of([2])
+    kw = dict(contextual_len=0, K1=4, K2=0, alpha=0.1, N=1.0)
+    with pytest.raises(TypeError):
+        cache.attend(q.float(), k, v, offs, None, pages, t, **kw)
+    with pytest.raises(TypeError):
+        cache.attend(q, k, v, offs.long(), None, pages, t, **kw)
+    with pytest.raises(ValueError):
+        cache.attend(q, k, v, offs_of([1, 1]), None, pages, t, **kw)
+    with pytest.raises(ValueError):
+        cache.attend(q, None, None, offs, dev32([1]), pages, t, **kw)
+    with pytest.raises(ValueError):
+        cache.attend(q[:, :1], k, v, offs, None, pages, t, **kw)
+    with pytest.raises(ValueError):
+        cache.attend(q.transpose(1, 2).contiguous().transpose(1, 2), k, v, offs, None, pages, t,
+                     **kw)
+    with pytest.raises(ValueError):
+        cache.append(k, v, torch.zeros(2, dtype=torch.int64, device=DEV), pages[:, :, :-16], t)
+    with pytest.raises(TypeError):
+        cache.append(k, v, torch.zeros(2, dtype=torch.int32, device=DEV), pages, t)
+    with pytest.raises(ValueError):
+        cache.append(k[:1], v, torch.zeros(2, dtype=torch.int64, device=DEV), pages, t)
+    with pytest.raises(ValueError):
+        cache.plan(t, offs, total_tokens=2, slots=torch.empty(3, dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError):
+        cache.CacheTables(t.buf[:40], 1, 2, 3, 16)
