@@ -138,7 +138,7 @@ int hstu_cache_read(const hstu_cache_tables* t, const hstu_cache_rows* r, hstu_s
  * and the others are its last history tokens, at positions
  * Lh - (n - num_targets[b]) .. Lh - 1.  With hstu_sla.h's mask,
  *     out_i = (1/N) sum_j M(i,j) SiLU(alpha q_i . k_j) v_j
- * over the cached k_j, v_j (m + s code, not rounded), a history row's own pair
+ * over the cached k_j, v_j (m + s code), a history row's own pair
  * among them; a candidate's own pair uses its row of k and v.  A row that sees
  * nothing is zero.  Rows of out behind seq_offsets[B] are left as they were.
  *
@@ -167,8 +167,14 @@ typedef struct {
   int64_t out_row_stride;
 } hstu_cache_attend_params;
 
+/* Workspace of a call with these sizes (the blocks' partial sums): 256-byte
+ * aligned, contents need not be initialised; calls that may overlap need one
+ * each.  0 on invalid arguments. */
+size_t hstu_cache_attend_workspace_bytes(const hstu_cache_tables* t,
+                                         const hstu_cache_attend_params* p);
+
 int hstu_cache_attend(const hstu_cache_tables* t, const hstu_cache_attend_params* p,
-                      hstu_stream_t stream);
+                      void* workspace, size_t workspace_bytes, hstu_stream_t stream);
 
 /* Synchronises `stream` and returns the tables' status, or HSTU_SLA_ERR_CUDA. */
 int hstu_cache_get_error(const hstu_cache_tables* t, hstu_stream_t stream);

@@ -221,7 +221,10 @@ def load():
     lib.hstu_cache_append.restype = ctypes.c_int
     lib.hstu_cache_read.argtypes = [tab, ctypes.POINTER(CacheRows), vp]
     lib.hstu_cache_read.restype = ctypes.c_int
-    lib.hstu_cache_attend.argtypes = [tab, ctypes.POINTER(CacheAttendParams), vp]
+    att = ctypes.POINTER(CacheAttendParams)
+    lib.hstu_cache_attend_workspace_bytes.argtypes = [tab, att]
+    lib.hstu_cache_attend_workspace_bytes.restype = sz
+    lib.hstu_cache_attend.argtypes = [tab, att, vp, sz, vp]
     lib.hstu_cache_attend.restype = ctypes.c_int
     lib.hstu_cache_get_error.argtypes = [tab, vp]
     lib.hstu_cache_get_error.restype = ctypes.c_int

@@ -191,17 +191,24 @@ def plan(tables: CacheTables, seq_offsets: torch.Tensor, num_targets: Optional[t
     rel = _i32(release, tables.B, "release", dev)
     slots = _slots_out(slots, total_tokens, dev)
     lib = _abi.load()
-    need = lib.hstu_cache_plan_workspace_bytes(tables.B)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace must have {need} bytes on {dev}")
+    ws = _workspace(workspace, lib.hstu_cache_plan_workspace_bytes(tables.B), dev, stream)
     with _On(dev):
         _check(lib.hstu_cache_plan(tables._c, o, nt, rel, total_tokens, slots.data_ptr(),
-                                   workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(),
-                                   _stream(stream, dev)), "hstu_cache_plan")
+                                   ws.data_ptr(), ws.numel(), _stream(stream, dev)), "hstu_cache_plan")
     return slots
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, dev, stream) -> torch.Tensor:
+    """The given workspace, checked, or a new one (kept from reuse until
+    `stream`, if another than the current one, is done with it)."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or \
+            not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
+    return workspace
 
 
 def _slots_out(slots, total_tokens, dev):
@@ -275,7 +282,7 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
            seq_offsets: torch.Tensor, num_targets: Optional[torch.Tensor], pages: torch.Tensor,
            tables: CacheTables, *, contextual_len: int, K1: int, K2: int, alpha: float, N: float,
            max_new: Optional[int] = None, out: Optional[torch.Tensor] = None,
-           stream=None) -> torch.Tensor:
+           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """SLA HSTU attention of the step's rows over the cached histories; returns
     out [T, H, d] bf16 (rows behind seq_offsets[B] are left as they were).  The
     step's history rows are in the cache already (plan, append); a candidate
@@ -301,9 +308,11 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
         _i32(num_targets, tables.B, "num_targets", dev), int(contextual_len), int(K1), int(K2),
         float(alpha), float(N), q.data_ptr(), k_ptr, v_ptr, q_rs, k_rs, v_rs, pages.data_ptr(),
         stride, out.data_ptr(), _rows(out, "out", T, H, d, dev))
+    lib = _abi.load()
+    ws = _workspace(workspace, lib.hstu_cache_attend_workspace_bytes(tables._c, p), dev, stream)
     with _On(dev):
-        _check(_abi.load().hstu_cache_attend(tables._c, p, _stream(stream, dev)),
-               "hstu_cache_attend")
+        _check(lib.hstu_cache_attend(tables._c, p, ws.data_ptr(), ws.numel(),
+                                     _stream(stream, dev)), "hstu_cache_attend")
     return out
 
 

@@ -79,6 +79,47 @@ int rows_args(const hstu_cache_tables* t, const hstu_cache_rows* r, CacheRowArgs
   return HSTU_SLA_OK;
 }
 
+int attend_args(const hstu_cache_tables* t, const hstu_cache_attend_params* p, CacheAttnArgs* out) {
+  CacheAttnArgs& a = *out;
+  memset(&a, 0, sizeof(a));
+  int e = make_tab(t, &a.t);
+  if (e) return e;
+  if (p == nullptr || p->seq_offsets == nullptr) return HSTU_SLA_ERR_INVALID_ARG;
+  if ((e = check_heads(p->H, p->d, p->total_tokens))) return e;
+  if (p->max_new < 0 || p->K1 < 0 || p->K2 < 0 || p->contextual_len < 0)
+    return HSTU_SLA_ERR_INVALID_ARG;
+  if (!(p->N > 0.f) || !isfinite(p->N) || !isfinite(p->alpha)) return HSTU_SLA_ERR_INVALID_ARG;
+  if ((e = check_pages(p->pages, p->page_stride, p->H, p->d, t->page_size))) return e;
+  if (p->total_tokens > 0) {
+    if ((e = check_rows(p->q, p->q_row_stride, p->H, p->d))) return e;
+    if ((e = check_rows(p->out, p->out_row_stride, p->H, p->d))) return e;
+    if (p->num_targets) {
+      if ((e = check_rows(p->k, p->k_row_stride, p->H, p->d))) return e;
+      if ((e = check_rows(p->v, p->v_row_stride, p->H, p->d))) return e;
+    }
+  }
+  a.H = p->H;
+  a.max_new = (int)(p->max_new < p->total_tokens ? p->max_new : p->total_tokens);
+  a.T = p->total_tokens;
+  a.offs = p->seq_offsets;
+  a.nts = p->num_targets;
+  a.K1 = p->K1;
+  a.K2e = p->K2 > p->contextual_len ? p->K2 : p->contextual_len;
+  a.alpha = p->alpha;
+  a.inv_n = 1.0f / p->N;
+  a.q = static_cast<const bf16*>(p->q);
+  a.k = static_cast<const bf16*>(p->k);
+  a.v = static_cast<const bf16*>(p->v);
+  a.q_rs = p->q_row_stride;
+  a.k_rs = p->k_row_stride;
+  a.v_rs = p->v_row_stride;
+  a.pages = static_cast<const uint8_t*>(p->pages);
+  a.page_stride = p->page_stride;
+  a.out = static_cast<bf16*>(p->out);
+  a.o_rs = p->out_row_stride;
+  return HSTU_SLA_OK;
+}
+
 int status_of(cudaError_t e) { return e == cudaSuccess ? HSTU_SLA_OK : HSTU_SLA_ERR_CUDA; }
 
 }  // namespace
@@ -131,46 +172,22 @@ int hstu_cache_read(const hstu_cache_tables* t, const hstu_cache_rows* r, hstu_s
   return status_of(launch_cache_read(a, r->d, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int hstu_cache_attend(const hstu_cache_tables* t, const hstu_cache_attend_params* p,
-                      hstu_stream_t stream) {
+size_t hstu_cache_attend_workspace_bytes(const hstu_cache_tables* t,
+                                         const hstu_cache_attend_params* p) {
   CacheAttnArgs a;
-  memset(&a, 0, sizeof(a));
-  int e = make_tab(t, &a.t);
+  return attend_args(t, p, &a) ? 0 : cache_attend_ws_bytes(a, p->d);
+}
+
+int hstu_cache_attend(const hstu_cache_tables* t, const hstu_cache_attend_params* p,
+                      void* workspace, size_t workspace_bytes, hstu_stream_t stream) {
+  CacheAttnArgs a;
+  const int e = attend_args(t, p, &a);
   if (e) return e;
-  if (p == nullptr || p->seq_offsets == nullptr) return HSTU_SLA_ERR_INVALID_ARG;
-  if ((e = check_heads(p->H, p->d, p->total_tokens))) return e;
-  if (p->max_new < 0 || p->K1 < 0 || p->K2 < 0 || p->contextual_len < 0)
-    return HSTU_SLA_ERR_INVALID_ARG;
-  if (!(p->N > 0.f) || !isfinite(p->N) || !isfinite(p->alpha)) return HSTU_SLA_ERR_INVALID_ARG;
-  if ((e = check_pages(p->pages, p->page_stride, p->H, p->d, t->page_size))) return e;
-  if (p->total_tokens > 0) {
-    if ((e = check_rows(p->q, p->q_row_stride, p->H, p->d))) return e;
-    if ((e = check_rows(p->out, p->out_row_stride, p->H, p->d))) return e;
-    if (p->num_targets) {
-      if ((e = check_rows(p->k, p->k_row_stride, p->H, p->d))) return e;
-      if ((e = check_rows(p->v, p->v_row_stride, p->H, p->d))) return e;
-    }
-  }
-  a.H = p->H;
-  a.max_new = (int)(p->max_new < p->total_tokens ? p->max_new : p->total_tokens);
-  a.T = p->total_tokens;
-  a.offs = p->seq_offsets;
-  a.nts = p->num_targets;
-  a.K1 = p->K1;
-  a.K2e = p->K2 > p->contextual_len ? p->K2 : p->contextual_len;
-  a.alpha = p->alpha;
-  a.inv_n = 1.0f / p->N;
-  a.q = static_cast<const bf16*>(p->q);
-  a.k = static_cast<const bf16*>(p->k);
-  a.v = static_cast<const bf16*>(p->v);
-  a.q_rs = p->q_row_stride;
-  a.k_rs = p->k_row_stride;
-  a.v_rs = p->v_row_stride;
-  a.pages = static_cast<const uint8_t*>(p->pages);
-  a.page_stride = p->page_stride;
-  a.out = static_cast<bf16*>(p->out);
-  a.o_rs = p->out_row_stride;
-  return status_of(launch_cache_attend(a, p->d, reinterpret_cast<cudaStream_t>(stream)));
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < cache_attend_ws_bytes(a, p->d))
+    return HSTU_SLA_ERR_WORKSPACE;
+  return status_of(
+      launch_cache_attend(a, p->d, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int hstu_cache_get_error(const hstu_cache_tables* t, hstu_stream_t stream) {

@@ -7,30 +7,38 @@
 // applied to the scores and the probabilities, where they are one per key:
 //   q . k_j = s_j (q . c_j) + m_j sum(q)
 //   out     = sum_j (P_ij s_j) c_j + sum_j P_ij m_j.
-// A nibble becomes the bf16 value 16 + c by one shift and one and-or (bits 3..6
-// of 16.0's mantissa), so the 16s are taken off in the same two places:
-//   x_j  = s_j (q . (16 + c_j)) + (m_j - 16 s_j) sum(q)
-//   out  = sum_j P'_j (16 + c_j) + sum_j (P_j m_j - 16 P'_j),  P' = bf16(P s).
-// P' is the only rounding to fewer bits than fp32 (the matrix instruction takes
-// bf16), and its 16 is taken off as rounded, so it costs one bf16 rounding of
-// P_j s_j against c_j, no more.  Masked pairs are selected to zero before any
-// product, so nothing in a masked place reaches a row.
+// A nibble c in bits 0..3 of a 16-bit half is the f16 number c 2^-24 as it
+// stands, and one in bits 4..7 is 16 c 2^-24 (both subnormal, exact, and taken
+// at full rate by the matrix instructions): one and per pair of values, one
+// shift per word.  The factors 16 go into q (its dims of those nibbles enter
+// divided by 16) and into the output's factor.
 //
-// A unit is one (sequence, head, 16 rows); its key tiles of 64 tokens are split
-// over a cluster of S blocks and there over the warps.  Each warp streams its
-// tiles through its own ring of bulk copies (one per page: a head's codes and
-// pairs of a page are contiguous) and keeps everything in registers: S by
-// m16n8k16 with the codes as B operand, P, and O += P' V the same way.  SiLU
-// attention has no softmax, so partial results only add: warps through shared
-// memory, blocks through distributed shared memory, both in a fixed order.
+// Roundings to fewer bits than fp32: q enters as f16 times a power of two that
+// puts the row's largest |q| into [2^14, 2^15): bf16's 8 bits fit f16's 11, so
+// this is exact down to 2^-27 of that largest.  P s enters as f16 times a power
+// of two per row, taken from the row's first tile and lowered if a later tile
+// would overflow (the sums are then scaled down with it): 11 bits, and what is
+// more than 2^18 below that tile's largest is held to 2^-29 of it.  Masked pairs
+// are selected to zero before any product, so nothing in a masked place reaches
+// a row.
 //
-// Which key a matrix column stands for is free, so it is chosen for the loads:
-// columns 2t, 2t + 1 of score tiles (u, 0) and (u, 1) are tokens 16 t + 4 u
-// + {0, 1} and {2, 3}; a thread's K bytes (its quarter of d) and V bytes (16
-// tokens of a dim pair) are then single 16-byte loads, without bank conflicts.
+// A unit is one (sequence, head, 8 rows); its key tiles of 64 tokens are split
+// over S blocks and there over the warps.  A block streams its tiles through a
+// ring of bulk copies (one per page: a head's codes and pairs of a page are
+// contiguous); a warp takes a whole tile and keeps everything in registers: S
+// as [keys][rows] and O as [dims][rows], P turned in between by one register
+// transpose per 8 x 8.  SiLU attention has no softmax, so partial results only
+// add: warps through shared memory, blocks through the workspace and a second
+// kernel, in a fixed order.
 //
-// Bound: HBM for long histories (d + 8 bytes per token and head).
-#include <cooperative_groups.h>
+// Which key a matrix row stands for is free, so it is chosen for the loads:
+// rows g and g + 8 of score tile u are tokens 16 (g / 2) + 4 u + g mod 2 and two
+// further on; a thread's K bytes (its quarter of d) and V bytes (16 tokens of a
+// dim pair) are then single 16-byte loads, without bank conflicts.
+//
+// Bound: HBM for long histories (d + 8 bytes per token and head); instructions
+// come next, above all the two per pair of codes.
+#include <cuda_fp16.h>
 
 #include "cache_common.cuh"
 #include "sm100.cuh"
@@ -40,9 +48,8 @@ namespace hstu {
 namespace {
 
 using namespace sm100;
-namespace cg = cooperative_groups;
 
-constexpr int kW = 4, kThreads = 32 * kW, kRows = 16, kTK = 64, kStages = 2;
+constexpr int kW = 8, kThreads = 32 * kW, kRows = 8, kTK = 64, kStages = 12;
 
 template <int D>
 struct StepCfg {
@@ -50,10 +57,13 @@ struct StepCfg {
   // further apart when there are several, so that a warp's V loads from them
   // fall into different banks
   static constexpr int STG = kTK * (D + 8) + 128;
-  static constexpr int OFF_SELF = kW * kStages * STG;
+  static constexpr int PITCH = D + 8;               // floats between rows of a result
+  static constexpr int OFF_REST = kStages * STG;    // [warp][8]
+  static constexpr int OFF_SELF = OFF_REST + kW * kRows * 4;
   static constexpr int OFF_BAR = OFF_SELF + kRows * 4;
-  static constexpr int SMEM = OFF_BAR + kW * kStages * 8;
-  static_assert(kStages * STG >= kRows * D * 4, "a warp's result fits its ring");
+  static constexpr int OFF_GEN = OFF_BAR + kStages * 8;  // phase a stage is armed for
+  static constexpr int SMEM = OFF_GEN + kStages * 4;
+  static_assert(kStages * STG >= kW * kRows * PITCH * 4, "the warps' results fit the ring");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -78,21 +88,38 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, cons
   return true;
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-      " {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// Waits, as long at most, until *gen is n.
+__device__ __forceinline__ bool bounded_armed(const volatile int* gen, int n, const CacheTab& t) {
+  if (*gen == n) return true;
+  const uint64_t t0 = globaltimer();
+  while (*gen != n) {
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      cache_fail(t, HSTU_SLA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
 }
 
-// Nibbles P and P + 4 of w as a bf16 pair 16 + c.
-template <int P>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  const uint32_t x = P == 0 ? w << 3 : w >> (4 * P - 3);
-  return (x & 0x00780078u) | 0x41804180u;
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
+      " {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;  // nibbles n, n + 4 as f16 codes
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -109,105 +136,14 @@ __device__ __forceinline__ void lds(uint32_t (&r)[N], uint32_t addr) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
 }
 
+// Tiles of one block of a unit with n of them: at least one per warp.
+__device__ __forceinline__ int block_tiles(int n, int S) { return imax(kW, (n + S - 1) / S); }
+
+// A candidate's own pair, SiLU(alpha q_i . k_i), of rows r0 + warp, ...
 template <int D>
-__global__ void __launch_bounds__(kThreads, 3)
-    cache_step_kernel(const __grid_constant__ CacheAttnArgs a, int S, int row_tiles) {
-  using C = StepCfg<D>;
-  constexpr int KS = D / 16, WD = D / 32;  // k-steps of q . k, words of a thread's K quarter
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int split = (int)blockIdx.x % S;
-  const int unit = (int)blockIdx.x / S;
-  const int bh = unit / row_tiles, r0 = (unit % row_tiles) * kRows;
-  const int b = bh / a.H, h = bh % a.H;
-
-  // (every block of a cluster takes the same way out)
-  CacheSeq sq;
-  if (!cache_seq(a, b, &sq) || r0 >= sq.n) return;
-  const int nr = imin(kRows, sq.n - r0);
-  CacheTiles tl = cache_tiles<kTK>(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
-  if (cache_status(a.t) != 0) tl.n = 0;
-  const int e0 = (int)((int64_t)tl.n * split / S), e1 = (int)((int64_t)tl.n * (split + 1) / S);
-  const int mine = e0 + warp < e1 ? (e1 - e0 - warp + kW - 1) / kW : 0;  // this warp's tiles
-
-  const int ps = a.t.ps, lps = a.t.lps, ppt = kTK >> lps;  // pages a tile
-  const PageLayout<D> lay(ps);
-  const int pitch = lay.bytes + (ps < kTK ? 2 * ps : 0);
-  const uint32_t ring = smem_addr(smem) + warp * kStages * C::STG;
-  const uint32_t bar = smem_addr(smem) + C::OFF_BAR + warp * kStages * 8;
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
-    fence_barrier_init();
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  __syncwarp();
-
-  // Page ids of tiles k0 + lane of this warp, 32 tiles at a time.
-  const int32_t* bt = a.t.bt + (int64_t)b * a.t.M;
-  const int pages = (sq.Lh + ps - 1) >> lps;
-  int id[4];
-  auto load_ids = [&](int k0) {
-    const int e = e0 + warp + (k0 + lane) * kW;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      id[p] = 0;
-      if (p < ppt && e < e1) {
-        const int i = tl.at(e) * ppt + p;
-        if (i < pages) {
-          id[p] = bt[i];
-          if (id[p] < 0 || id[p] >= a.t.P) {
-            cache_fail(a.t, HSTU_SLA_ERR_BAD_INPUT);
-            id[p] = 0;
-          }
-        }
-      }
-    }
-  };
-  auto issue = [&](int k) {
-    if ((k & 31) == 0) load_ids(k);
-    const int s = k % kStages;
-    const int first = tl.at(e0 + warp + k * kW) * ppt;
-    const int np = imin(ppt, pages - first);
-    if (lane == 0) mbar_expect_tx(bar + 8 * s, (uint32_t)(np * lay.bytes));
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int page = __shfl_sync(0xffffffffu, id[p], k & 31);
-      if (lane == 0 && p < np)
-        bulk_load(ring + s * C::STG + p * pitch,
-                  a.pages + page * a.page_stride + (int64_t)h * lay.bytes, (uint32_t)lay.bytes,
-                  bar + 8 * s);
-    }
-  };
-  for (int k = 0; k < kStages && k < mine; ++k) issue(k);
-
-  // Q fragments: k index 2t + {0, 1} (+ 8) of k-step ks is dim t D/4 + 4 ks +
-  // {0, 1} ({2, 3}).  sum(q) of rows g and g + 8.
-  uint32_t qf[KS][4];
-  float sum0 = 0.f, sum1 = 0.f;
-  const bool two = nr > 8;
-  {
-    const bf16* q0 = a.q + (int64_t)(sq.s0 + r0 + g) * a.q_rs + h * D + t * (D / 4);
-    const bf16* q1 = q0 + 8 * a.q_rs;
-#pragma unroll
-    for (int ks = 0; ks < KS; ks += 2) {
-      uint4 x = make_uint4(0, 0, 0, 0), y = x;
-      if (g < nr) x = *reinterpret_cast<const uint4*>(q0 + 4 * ks);
-      if (g + 8 < nr) y = *reinterpret_cast<const uint4*>(q1 + 4 * ks);
-      qf[ks][0] = x.x; qf[ks][2] = x.y; qf[ks + 1][0] = x.z; qf[ks + 1][2] = x.w;
-      qf[ks][1] = y.x; qf[ks][3] = y.y; qf[ks + 1][1] = y.z; qf[ks + 1][3] = y.w;
-      sum0 += (bf_lo(x.x) + bf_hi(x.x)) + (bf_lo(x.y) + bf_hi(x.y)) +
-              ((bf_lo(x.z) + bf_hi(x.z)) + (bf_lo(x.w) + bf_hi(x.w)));
-      sum1 += (bf_lo(y.x) + bf_hi(y.x)) + (bf_lo(y.y) + bf_hi(y.y)) +
-              ((bf_lo(y.z) + bf_hi(y.z)) + (bf_lo(y.w) + bf_hi(y.w)));
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      sum0 += __shfl_xor_sync(0xffffffffu, sum0, o);
-      sum1 += __shfl_xor_sync(0xffffffffu, sum1, o);
-    }
-  }
-  // A candidate's own pair: SiLU(alpha q_i . k_i), by a warp per row.
-  float* self = reinterpret_cast<float*>(smem + C::OFF_SELF);
+__device__ __forceinline__ void self_pairs(const CacheAttnArgs& a, const CacheSeq& sq, int h,
+                                           int r0, int nr, float* self) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int r = warp; r < nr; r += kW) {
     float p = 0.f;
     if (r0 + r >= sq.h) {
@@ -223,205 +159,449 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     if (lane == 0) self[r] = p;
   }
+}
 
-  const CacheRow c0 = cache_row(r0 + imin(g, nr - 1), sq.h, sq.Lh, a.K1, a.K2e);
-  const CacheRow c1 = cache_row(r0 + imin(g + 8, nr - 1), sq.h, sq.Lh, a.K1, a.K2e);
-  const CacheFull whole = cache_full(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
-  const float ha = 0.5f * a.alpha;
+// Dims c, c + 1 of row r: the sum over keys, the own pair, 1/N, bf16.
+__device__ __forceinline__ void store_pair(const CacheAttnArgs& a, const CacheSeq& sq, int col,
+                                           int r, float2 x, float self) {
+  const int64_t row = sq.s0 + r;
+  if (r >= sq.h) {
+    const uint32_t v2 = *reinterpret_cast<const uint32_t*>(a.v + row * a.v_rs + col);
+    x.x = fmaf(self, bf_lo(v2), x.x);
+    x.y = fmaf(self, bf_hi(v2), x.y);
+  }
+  *reinterpret_cast<uint32_t*>(a.out + row * a.o_rs + col) =
+      pack_bf16x2(x.x * a.inv_n, x.y * a.inv_n);
+}
 
-  float o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float rest0 = 0.f, rest1 = 0.f;  // sum P m - 16 P' of rows g, g + 8 (this thread's keys)
+// parts: fp32 [unit][S][8][D], the blocks' sums (S > 1 only).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    cache_step_kernel(const __grid_constant__ CacheAttnArgs a, int S, int row_tiles,
+                      float* __restrict__ parts) {
+  using C = StepCfg<D>;
+  constexpr int WD = D / 32;  // words of a thread's K quarter
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int split = (int)blockIdx.x % S;
+  const int unit = (int)blockIdx.x / S;
+  const int bh = unit / row_tiles, r0 = (unit % row_tiles) * kRows;
+  const int b = bh / a.H, h = bh % a.H;
 
-  const int pt = (16 * t) >> lps, in = (16 * t) & (ps - 1);    // page and place of tokens 16 t
-  const int pg = (16 * (g >> 1)) >> lps, ing = (16 * (g >> 1)) & (ps - 1);
-  bool ok = true;
-  int k = 0;
-  for (; k < mine; ++k) {
-    const int s = k % kStages;
-    ok = __all_sync(0xffffffffu, bounded_wait(bar + 8 * s, (k / kStages) & 1, a.t));
-    if (!ok) break;
-    const int j0 = tl.at(e0 + warp + k * kW) * kTK;
-    const bool full = whole(j0, kTK);
-    const uint32_t stg = ring + s * C::STG;
-    const uint32_t kbase = stg + pg * pitch + (ing + (g & 1)) * (D / 2) + t * (D / 8);
-    const uint32_t par = stg + pt * pitch + lay.kp + 4 * in;
-    uint32_t pf[4][4];
+  CacheSeq sq;
+  if (!cache_seq(a, b, &sq) || r0 >= sq.n || cache_status(a.t) != 0) return;
+  const int nr = imin(kRows, sq.n - r0);
+  const CacheTiles tl = cache_tiles<kTK>(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
+  const int bl = block_tiles(tl.n, S);
+  const int e0 = imin(split * bl, tl.n), nt = imin(bl, tl.n - e0);  // this block's tiles
+  if (split > 0 && nt <= 0) return;
+
+  const int ps = a.t.ps, lps = a.t.lps, ppt = kTK >> lps;  // pages a tile
+  const PageLayout<D> lay(ps);
+  const int pitch = lay.bytes + (ps < kTK ? 2 * ps : 0);
+  const uint32_t ring = smem_addr(smem), bar = ring + C::OFF_BAR;
+  volatile int* gen = reinterpret_cast<volatile int*>(smem + C::OFF_GEN);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
+    fence_barrier_init();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+
+  // The block's tiles k = 0, 1, ... use stage k mod kStages; warp k mod kW
+  // consumes tile k and then loads tile k + kStages into the stage it freed.
+  // The first kStages tiles are loaded by the warps in turn, so a warp loads
+  // tiles warp, warp + kW (if below kStages), then its own + kStages.
+  // Page ids of the tiles a warp consumes later are held 32 at a time, one per
+  // lane: entry i is tile kStages + warp + i kW.
+  const int32_t* bt = a.t.bt + (int64_t)b * a.t.M;
+  const int pages = (sq.Lh + ps - 1) >> lps;
+  auto page_id = [&](int k, int p) -> int {
+    if (k >= nt || p >= ppt) return 0;
+    const int i = tl.at(e0 + k) * ppt + p;
+    if (i >= pages) return 0;
+    const int x = bt[i];
+    if (x >= 0 && x < a.t.P) return x;
+    cache_fail(a.t, HSTU_SLA_ERR_BAD_INPUT);
+    return 0;
+  };
+  auto load = [&](int k, const int (&id)[4]) {  // by one lane
+    const uint32_t dst = ring + (k % kStages) * C::STG, bk = bar + 8 * (k % kStages);
+    const int np = imin(ppt, pages - tl.at(e0 + k) * ppt);
+    mbar_expect_tx(bk, (uint32_t)(np * lay.bytes));
+    __threadfence_block();
+    gen[k % kStages] = k / kStages;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t ka[WD], kb[WD];
-      lds<WD>(ka, kbase + 4 * u * (D / 2));
-      lds<WD>(kb, kbase + (4 * u + 2) * (D / 2));
+    for (int p = 0; p < 4; ++p)
+      if (p < np)
+        bulk_load(dst + p * pitch, a.pages + id[p] * a.page_stride + (int64_t)h * lay.bytes,
+                  (uint32_t)lay.bytes, bk);
+  };
+  {
+    // lanes 0, 1: the warp's first loads; lane 2 on: entry lane - 2 would wait
+    int id[4];
+    const int k = warp + lane * kW;
+    const bool mine = k < kStages && k < nt;
+    if (mine) {
 #pragma unroll
-      for (int w = 0; w < WD; ++w) {
-        mma16816(sa, qf[2 * w], code_pair<0>(ka[w]), code_pair<1>(ka[w]));
-        mma16816(sb, qf[2 * w], code_pair<0>(kb[w]), code_pair<1>(kb[w]));
-        mma16816(sa, qf[2 * w + 1], code_pair<2>(ka[w]), code_pair<3>(ka[w]));
-        mma16816(sb, qf[2 * w + 1], code_pair<2>(kb[w]), code_pair<3>(kb[w]));
-      }
-      uint32_t kp[4], vp[4];
-      lds<4>(kp, par + 16 * u);
-      lds<4>(vp, par + 16 * u + (lay.vp - lay.kp));
-      float p0[4], p1[4];
-      const int j = j0 + 16 * t + 4 * u;
+      for (int p = 0; p < 4; ++p) id[p] = page_id(k, p);
+    }
+    __syncthreads();  // barriers are initialised
+    if (mine) load(k, id);
+  }
+  int id[4];
+  auto load_ids = [&](int i0) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) id[p] = page_id(kStages + warp + (i0 + lane) * kW, p);
+  };
+  load_ids(0);
+
+  // Q fragments of row g: this thread's quarter of its dims, in the order of a
+  // K word's pairs, every second one divided by 16.  sum(q) alpha / 2, and the
+  // factor that makes the matrix product alpha / 2 q . c.
+  uint32_t qf[2 * WD][2];
+  float sum0, sum1, f0, f1;  // of rows 2t, 2t + 1
+  {
+    uint32_t x[WD][4];
+    uint32_t most = 0;
+    float sum = 0.f;
+    const bf16* q0 = a.q + (int64_t)(sq.s0 + r0 + g) * a.q_rs + h * D + t * (D / 4);
+#pragma unroll
+    for (int w = 0; w < WD; ++w) {
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (g < nr) y = *reinterpret_cast<const uint4*>(q0 + 8 * w);
+      x[w][0] = y.x; x[w][1] = y.y; x[w][2] = y.z; x[w][3] = y.w;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float ks = bf_lo(kp[e]) * ha, km = fmaf(ks, -16.f, bf_hi(kp[e]) * ha);
-        const float x0 = fmaf(e < 2 ? sa[e] : sb[e - 2], ks, km * sum0);
-        p0[e] = fmaf(x0, tanh_approx(x0), x0);
-        if (two) {
-          const float x1 = fmaf(e < 2 ? sa[e + 2] : sb[e], ks, km * sum1);
-          p1[e] = fmaf(x1, tanh_approx(x1), x1);
-        } else {
-          p1[e] = 0.f;
-        }
-      }
-      float q0[4], q1[4], m0[4], m1[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float vs = bf_lo(vp[e]), vm = bf_hi(vp[e]);
-        q0[e] = p0[e] * vs;
-        m0[e] = p0[e] * vm;
-        q1[e] = two ? p1[e] * vs : 0.f;
-        m1[e] = two ? p1[e] * vm : 0.f;
-        if (!full) {
-          const bool see0 = j + e < c0.pre || (j + e >= c0.lo && j + e < c0.hi);
-          const bool see1 = j + e < c1.pre || (j + e >= c1.lo && j + e < c1.hi);
-          q0[e] = see0 ? q0[e] : 0.f;
-          m0[e] = see0 ? m0[e] : 0.f;
-          q1[e] = see1 ? q1[e] : 0.f;
-          m1[e] = see1 ? m1[e] : 0.f;
-        }
-      }
-      pf[u][0] = pack_bf16x2(q0[0], q0[1]);
-      pf[u][1] = pack_bf16x2(q1[0], q1[1]);
-      pf[u][2] = pack_bf16x2(q0[2], q0[3]);
-      pf[u][3] = pack_bf16x2(q1[2], q1[3]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t w0 = pf[u][e < 2 ? 0 : 2], w1 = pf[u][e < 2 ? 1 : 3];
-        rest0 += fmaf(e & 1 ? bf_hi(w0) : bf_lo(w0), -16.f, m0[e]);
-        if (two) rest1 += fmaf(e & 1 ? bf_hi(w1) : bf_lo(w1), -16.f, m1[e]);
+        sum += bf_lo(x[w][e]) + bf_hi(x[w][e]);
+        most = umax(most, umax(x[w][e] & 0x7fffu, (x[w][e] >> 16) & 0x7fffu));
       }
     }
-    const uint32_t vbase = stg + pt * pitch + lay.v + in + g * ps;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      most = umax(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    // 2^(14 - e) for a largest value in [2^e, 2^(e + 1)); rows of zeros and of
+    // values below 2^-112 take 2^126
+    const int e = imax((int)(most >> 7) - 127, -112);
+    const float up = __int_as_float((141 - e) << 23), down = __int_as_float((113 + e) << 23);
+    const float f = down * (0.5f * a.alpha * 16777216.f);
+    sum *= 0.5f * a.alpha;
+    if (most >= 0x7f80u) sum = __int_as_float(0x7fc00000);  // a NaN or infinity: a NaN row
+#pragma unroll
+    for (int w = 0; w < WD; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float z = i & 1 ? up * 0.0625f : up;
+        qf[2 * w + (i >> 1)][i & 1] = pack_f16(bf_lo(x[w][i]) * z, bf_hi(x[w][i]) * z);
+      }
+    sum0 = __shfl_sync(0xffffffffu, sum, 8 * t);
+    sum1 = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+    f0 = __shfl_sync(0xffffffffu, f, 8 * t);
+    f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+  }
+  const bool one = nr == 1;  // rows 2t + 1 do not exist
+  const CacheRow cr0 = cache_row(r0 + imin(2 * t, nr - 1), sq.h, sq.Lh, a.K1, a.K2e);
+  const CacheRow cr1 = cache_row(r0 + imin(2 * t + 1, nr - 1), sq.h, sq.Lh, a.K1, a.K2e);
+  const CacheFull whole = cache_full(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
+
+  // o[i]: dims 16 i + 2 g (+ 1 in [2], [3], times 16) of rows 2t ([0], [2]) and
+  // 2t + 1, times 2^-24 and the row's scale
+  float o[D / 16][4];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float rest0 = 0.f, rest1 = 0.f;    // sum P m of rows 2t, 2t + 1 (this thread's keys)
+  float sc0 = 0x1p100f, sc1 = sc0;   // the rows' scales: the first P lowers them
+
+  const int pt = (16 * t) >> lps, in = (16 * t) & (ps - 1);    // page and place of tokens 16 t
+  const int pg = (16 * (g >> 1)) >> lps, ing = (16 * (g >> 1)) & (ps - 1);  // and 16 (g / 2)
+  const uint32_t koff = pg * pitch + (ing + (g & 1)) * (D / 2) + t * (D / 8);
+  const uint32_t poff = pg * pitch + lay.kp + 4 * (ing + (g & 1));
+  const uint32_t voff = pt * pitch + lay.v + in + g * ps;
+  const int jg = 16 * (g >> 1) + (g & 1);
+  // Tile k is phase n = k / kStages of its stage's barrier.  A wait names only
+  // the parity of a phase, and phase n - 1 is another warp's tile, perhaps not
+  // landed yet: so first the stage has to be armed for phase n, which the warp
+  // that loads into it writes down.
+  auto landed = [&](int k) -> bool {
+    const int s = k % kStages, n = k / kStages;
+    bool done = n == 0 || bounded_armed(gen + s, n, a.t);
+    done = done && bounded_wait(bar + 8 * s, n & 1, a.t);
+    return __all_sync(0xffffffffu, done);
+  };
+  bool ok = true;
+  int k = warp, n_done = 0;
+  for (; k < nt; k += kW, ++n_done) {
+    ok = landed(k);
+    if (!ok) break;
+    const int j0 = tl.at(e0 + k) * kTK;
+    const uint32_t stg = ring + (k % kStages) * C::STG;
+    float p0[4][2], p1[4][2];  // P s of rows 2t, 2t + 1 at tokens j0 + jg + 4u (+ 2)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float st[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t ka[WD], kb[WD], kp[2], vp[2];
+      lds<WD>(ka, stg + koff + 4 * u * (D / 2));
+      lds<WD>(kb, stg + koff + (4 * u + 2) * (D / 2));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t x[1];
+        lds<1>(x, stg + poff + 16 * u + 8 * e);
+        kp[e] = x[0];
+        lds<1>(x, stg + poff + (lay.vp - lay.kp) + 16 * u + 8 * e);
+        vp[e] = x[0];
+      }
+#pragma unroll
+      for (int w = 0; w < WD; ++w) {
+        mma_f16(st, ka[w] & kLow, kb[w] & kLow, ka[w] & kHigh, kb[w] & kHigh, qf[2 * w][0],
+                qf[2 * w][1]);
+        const uint32_t x = ka[w] >> 8, y = kb[w] >> 8;
+        mma_f16(st, x & kLow, y & kLow, x & kHigh, y & kHigh, qf[2 * w + 1][0],
+                qf[2 * w + 1][1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ks = bf_lo(kp[e]), km = bf_hi(kp[e]), vs = bf_lo(vp[e]), vm = bf_hi(vp[e]);
+        const int j = j0 + jg + 4 * u + 2 * e;
+        float x = fmaf(st[2 * e] * f0, ks, km * sum0);
+        float p = fmaf(x, tanh_approx(x), x), m = p * vm;
+        p0[u][e] = p * vs;
+        if (!whole(j0, kTK)) {
+          const bool see = j < cr0.pre || (j >= cr0.lo && j < cr0.hi);
+          p0[u][e] = see ? p0[u][e] : 0.f;
+          m = see ? m : 0.f;
+        }
+        rest0 += m;
+        p1[u][e] = 0.f;
+        if (!one) {
+          x = fmaf(st[2 * e + 1] * f1, ks, km * sum1);
+          p = fmaf(x, tanh_approx(x), x);
+          m = p * vm;
+          p1[u][e] = p * vs;
+          if (!whole(j0, kTK)) {
+            const bool see = j < cr1.pre || (j >= cr1.lo && j < cr1.hi);
+            p1[u][e] = see ? p1[u][e] : 0.f;
+            m = see ? m : 0.f;
+          }
+          rest1 += m;
+        }
+      }
+    }
+    uint32_t pk[4][2];
+    uint32_t big = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        pk[u][e] = pack_f16(p0[u][e] * sc0, p1[u][e] * sc1);
+        big = __vmaxu2(big, pk[u][e] & 0x7fff7fffu);
+      }
+    if (__any_sync(0xffffffffu, (big & 0xffffu) >= 0x7c00u || big >= 0x7c000000u)) {
+      // P s beyond f16 with this scale (or the row's first): put its largest
+      // into [2^4, 2^5)
+      float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m0 = fmaxf(m0, fabsf(p0[u][e]));
+          m1 = fmaxf(m1, fabsf(p1[u][e]));
+        }
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
+        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
+      }
+      // 2^(4 - e): the exponent field of m is e + 127
+      auto scale = [](float m, float old) {
+        const int e = (int)(__float_as_uint(m) >> 23);
+        return e == 0 ? old : fminf(old, __int_as_float(imin(imax(258 - e, 4), 227) << 23));
+      };
+      const float n0 = scale(m0, sc0), n1 = scale(m1, sc1);
+      const float d0 = n0 / sc0, d1 = n1 / sc1;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        o[i][0] *= d0;
+        o[i][2] *= d0;
+        o[i][1] *= d1;
+        o[i][3] *= d1;
+      }
+      sc0 = n0;
+      sc1 = n1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) pk[u][e] = pack_f16(p0[u][e] * sc0, p1[u][e] * sc1);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      pk[u][0] = transpose8x8(pk[u][0]);
+      pk[u][1] = transpose8x8(pk[u][1]);
+    }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       uint32_t vw[4];
-      lds<4>(vw, vbase + 8 * i * ps);
+      lds<4>(vw, stg + voff + 8 * i * ps);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        // low nibbles: dim 2i; high: dim 2i + 1.  Bytes are tokens 0, 2, 1, 3.
-        mma16816(o[2 * i], pf[u], code_pair<0>(vw[u]), code_pair<2>(vw[u]));
-        mma16816(o[2 * i + 1], pf[u], code_pair<1>(vw[u]), code_pair<3>(vw[u]));
+        // low nibbles: dim 2 (8 i + g); high: the next.  Bytes are tokens 0, 2, 1, 3.
+        const uint32_t x = vw[u] >> 8;
+        mma_f16(o[i], vw[u] & kLow, vw[u] & kHigh, x & kLow, x & kHigh, pk[u][0], pk[u][1]);
       }
     }
     __syncwarp();
-    if (k + kStages < mine) issue(k + kStages);
+    if (n_done > 0 && (n_done & 31) == 0) load_ids(n_done);
+    if (k + kStages < nt) {
+      int x[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) x[p] = __shfl_sync(0xffffffffu, id[p], n_done & 31);
+      if (lane == 0) load(k + kStages, x);
+    }
   }
-  if (!ok) {  // copies in flight land before the ring is used again
-    for (int i = k; i < mine && i < k + kStages; ++i)
-      drain_wait(bar + 8 * (i % kStages), (i / kStages) & 1);
-    __syncwarp();
+  // If a wait gave up, the copies in flight land before the ring is used again
+  // or the block ends: of every stage, the phase that was armed last.
+  if (!__syncthreads_and(ok)) {
+    if (threadIdx.x < kStages) {
+      drain_wait(bar + 8 * threadIdx.x, 0);
+      drain_wait(bar + 8 * threadIdx.x, 1);
+    }
+    __syncthreads();
   }
 
-  // The warp's result into its ring, [16][D] fp32.
+  // The warp's result, [8][PITCH] fp32, and its rows' rest.
 #pragma unroll
-  for (int x = 1; x < 4; x <<= 1) {
+  for (int x = 4; x < 32; x <<= 1) {
     rest0 += __shfl_xor_sync(0xffffffffu, rest0, x);
     rest1 += __shfl_xor_sync(0xffffffffu, rest1, x);
   }
+  float* rests = reinterpret_cast<float*>(smem + C::OFF_REST);
+  float* self = reinterpret_cast<float*>(smem + C::OFF_SELF);
+  float* sums = reinterpret_cast<float*>(smem);
+  if (g == 0) {
+    rests[warp * kRows + 2 * t] = rest0;
+    rests[warp * kRows + 2 * t + 1] = rest1;
+  }
   {
-    // columns 2t, 2t + 1 of tile (2i + e) are dims 16 i + 4 t + e and + 2 + e
-    float* w = reinterpret_cast<float*>(smem + warp * kStages * C::STG);
+    const float i0 = 1.f / sc0, i1 = 1.f / sc1;  // exact: powers of two
+    float* w = sums + (warp * kRows + 2 * t) * C::PITCH + 2 * g;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      float4 x = make_float4(o[2 * i][0] + rest0, o[2 * i + 1][0] + rest0, o[2 * i][1] + rest0,
-                             o[2 * i + 1][1] + rest0);
-      *reinterpret_cast<float4*>(w + g * D + 16 * i + 4 * t) = x;
-      if (two) {
-        x = make_float4(o[2 * i][2] + rest1, o[2 * i + 1][2] + rest1, o[2 * i][3] + rest1,
-                        o[2 * i + 1][3] + rest1);
-        *reinterpret_cast<float4*>(w + (g + 8) * D + 16 * i + 4 * t) = x;
-      }
+      if (2 * t < nr)
+        *reinterpret_cast<float2*>(w + 16 * i) =
+            make_float2(o[i][0] * 0x1p24f * i0, o[i][2] * 0x1p20f * i0);
+      if (2 * t + 1 < nr)
+        *reinterpret_cast<float2*>(w + C::PITCH + 16 * i) =
+            make_float2(o[i][1] * 0x1p24f * i1, o[i][3] * 0x1p20f * i1);
     }
   }
+  if (S == 1) self_pairs<D>(a, sq, h, r0, nr, self);
   __syncthreads();
-  // sum of the block's warps, then of the cluster's blocks
-  // (in place of warp 0's: an element is read and written by one thread)
-  float* part = reinterpret_cast<float*>(smem);
   for (int e = threadIdx.x * 2; e < nr * D; e += 2 * kThreads) {
+    const int r = e / D, c = e % D;
     float2 x = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
-      const float2 y = *reinterpret_cast<const float2*>(smem + w * kStages * C::STG + 4 * e);
+      const float2 y =
+          *reinterpret_cast<const float2*>(sums + (w * kRows + r) * C::PITCH + c);
+      x.x += y.x + rests[w * kRows + r];
+      x.y += y.y + rests[w * kRows + r];
+    }
+    if (S == 1)
+      store_pair(a, sq, h * D + c, r0 + r, x, self[r]);
+    else
+      *reinterpret_cast<float2*>(parts + (int64_t)blockIdx.x * (kRows * D) + e) = x;
+  }
+}
+
+// The blocks' sums of a unit, in order.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    cache_join_kernel(const __grid_constant__ CacheAttnArgs a, int S, int row_tiles,
+                      const float* __restrict__ parts) {
+  __shared__ float self[kRows];
+  const int unit = blockIdx.x, bh = unit / row_tiles, r0 = (unit % row_tiles) * kRows;
+  const int b = bh / a.H, h = bh % a.H;
+  CacheSeq sq;
+  if (!cache_seq(a, b, &sq) || r0 >= sq.n || cache_status(a.t) != 0) return;
+  const int nr = imin(kRows, sq.n - r0);
+  const CacheTiles tl = cache_tiles<kTK>(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
+  const int used = imax(1, cdiv(tl.n, block_tiles(tl.n, S)));
+  self_pairs<D>(a, sq, h, r0, nr, self);
+  __syncthreads();
+  for (int e = threadIdx.x * 2; e < nr * D; e += 2 * kThreads) {
+    const float* p = parts + (int64_t)unit * S * (kRows * D) + e;
+    float2 x = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < used; ++i, p += kRows * D) {
+      const float2 y = *reinterpret_cast<const float2*>(p);
       x.x += y.x;
       x.y += y.y;
     }
-    *reinterpret_cast<float2*>(part + e) = x;
+    store_pair(a, sq, h * D + e % D, r0 + e / D, x, self[e / D]);
   }
-  cg::cluster_group cl = cg::this_cluster();
-  if (S > 1) cl.sync(); else __syncthreads();
-  for (int e = (split * kThreads + threadIdx.x) * 2; e < nr * D; e += 2 * kThreads * S) {
-    float2 x = *reinterpret_cast<const float2*>(S > 1 ? cl.map_shared_rank(part, 0) + e : part + e);
-    for (int r = 1; r < S; ++r) {
-      const float2 y = *reinterpret_cast<const float2*>(cl.map_shared_rank(part, r) + e);
-      x.x += y.x;
-      x.y += y.y;
-    }
-    const int r = e / D, c = e % D;
-    const int64_t row = sq.s0 + r0 + r;
-    if (r0 + r >= sq.h) {
-      const uint32_t v2 = *reinterpret_cast<const uint32_t*>(a.v + row * a.v_rs + h * D + c);
-      x.x = fmaf(self[r], bf_lo(v2), x.x);
-      x.y = fmaf(self[r], bf_hi(v2), x.y);
-    }
-    *reinterpret_cast<uint32_t*>(a.out + row * a.o_rs + h * D + c) =
-        pack_bf16x2(x.x * a.inv_n, x.y * a.inv_n);
-  }
-  if (S > 1) cl.sync();  // no block leaves while another reads its sum
+}
+
+// Blocks a unit.  Two blocks fit an SM.  A unit is split until the GPU is full
+// once, and further, down to 8 tiles a warp, until it is full eight times, so
+// that the last blocks to finish cost little of the whole (64 sequences x 4
+// heads of 8K-16K tokens, d = 128: 103 us unsplit, 92 in 4, 102 in 8; 10-tile
+// windows of the same batch: 10.3 us unsplit, 16.5 in 2).
+int step_splits(int64_t units, int64_t tiles) {
+  const int64_t slots = 2 * 148;
+  int64_t fill = (slots + units - 1) / units;
+  fill = fill < tiles / kW ? fill : tiles / kW;
+  int64_t even = tiles / (8 * kW);
+  even = even < slots * 8 / units ? even : slots * 8 / units;
+  const int64_t S = fill > even ? fill : even;
+  return S < 1 ? 1 : (int)S;
+}
+
+struct StepPlan {
+  int row_tiles, S;
+  int64_t units;
+};
+StepPlan step_plan(int B, int H, int max_new, int max_keys) {
+  StepPlan p;
+  p.row_tiles = (max_new + kRows - 1) / kRows;
+  p.units = (int64_t)B * H * p.row_tiles;
+  p.S = p.units > 0 ? step_splits(p.units, max_keys / kTK + 2) : 1;
+  return p;
+}
+
+// Most keys a row tile can meet.
+int most_keys(const CacheAttnArgs& a) {
+  const int64_t w = (int64_t)a.K1 + a.K2e + kRows, c = (int64_t)a.t.M * a.t.ps;
+  return (int)(w < c ? w : c);
 }
 
 template <int D>
-cudaError_t launch_step(const CacheAttnArgs& a, cudaStream_t st) {
+cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
   using C = StepCfg<D>;
-  auto kern = cache_step_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(
+      cache_step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const int row_tiles = (a.max_new + kRows - 1) / kRows;
-  const int64_t units = (int64_t)a.t.B * a.H * row_tiles;
-  // Blocks a unit: enough to fill the GPU about twice, no more than a unit has
-  // key tiles for (at least one per warp).
-  const int64_t keys =
-      imin(a.t.M * a.t.ps, (int)(((int64_t)a.K1 + a.K2e + kRows) < (1 << 30) ? a.K1 + a.K2e + kRows : 1 << 30));
-  const int64_t tiles = keys / kTK + 2;
-  int S = 1;
-  while (S < 8 && units * S < 2 * 148 && tiles >= 2 * S * kW) S *= 2;
-  if (units * S > 0x7fffffff) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * S));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, S, row_tiles);
+  const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
+  if (p.units * p.S > 0x7fffffff) return cudaErrorInvalidValue;
+  cache_step_kernel<D><<<(unsigned)(p.units * p.S), kThreads, C::SMEM, st>>>(a, p.S, p.row_tiles,
+                                                                           parts);
+  if (p.S > 1)
+    cache_join_kernel<D><<<(unsigned)p.units, kThreads, 0, st>>>(a, p.S, p.row_tiles, parts);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, cudaStream_t st) {
+size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d) {
+  const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
+  return p.S == 1 ? 256 : align256((size_t)p.units * p.S * kRows * d * sizeof(float));
+}
+
+cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st) {
   if (a.T == 0 || a.max_new == 0) return cudaSuccess;
-  if (d == 32) return launch_step<32>(a, st);
-  if (d == 64) return launch_step<64>(a, st);
-  return launch_step<128>(a, st);
+  float* parts = static_cast<float*>(ws);
+  if (d == 32) return launch_step<32>(a, parts, st);
+  if (d == 64) return launch_step<64>(a, parts, st);
+  return launch_step<128>(a, parts, st);
 }
 
 }  // namespace hstu

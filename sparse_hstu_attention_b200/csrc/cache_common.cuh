@@ -149,6 +149,7 @@ cudaError_t launch_cache_slot_map(const CacheTab& t, const int32_t* offs, int64_
                                   int64_t* slots, cudaStream_t st);
 cudaError_t launch_cache_append(const CacheRowArgs& a, int d, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheRowArgs& a, int d, cudaStream_t st);
-cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, cudaStream_t st);
+size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d);
+cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st);
 
 }  // namespace hstu

@@ -105,7 +105,8 @@ def test_bad_tables_are_refused(lib, field, value, code):
     assert lib.hstu_cache_slot_map(t, FAKE, 10, FAKE, None) == code
     assert lib.hstu_cache_append(t, _rows(), None) == code
     assert lib.hstu_cache_read(t, _rows(), None) == code
-    assert lib.hstu_cache_attend(t, _attend(), None) == code
+    assert lib.hstu_cache_attend(t, _attend(), FAKE, 1 << 30, None) == code
+    assert lib.hstu_cache_attend_workspace_bytes(t, _attend()) == 0
 
 
 def test_plan_refusals(lib):
@@ -147,7 +148,19 @@ def test_rows_refusals(lib, field, value, code):
     ("out_row_stride", 513, _abi.ERR_INVALID_ARG), ("pages", None, _abi.ERR_INVALID_ARG),
     ("total_tokens", 1 << 31, _abi.ERR_UNSUPPORTED)])
 def test_attend_refusals(lib, field, value, code):
-    assert lib.hstu_cache_attend(_tables(), _attend(**{field: value}), None) == code
+    p = _attend(**{field: value})
+    assert lib.hstu_cache_attend(_tables(), p, FAKE, 1 << 30, None) == code
+    assert lib.hstu_cache_attend_workspace_bytes(_tables(), p) == 0
+
+
+def test_attend_workspace_refusals(lib):
+    p = _attend()
+    need = lib.hstu_cache_attend_workspace_bytes(_tables(), p)
+    assert need >= 256 and need % 256 == 0
+    f = lib.hstu_cache_attend
+    assert f(_tables(), p, None, need, None) == _abi.ERR_WORKSPACE
+    assert f(_tables(), p, FAKE + 64, need, None) == _abi.ERR_WORKSPACE
+    assert f(_tables(), p, FAKE, need - 1, None) == _abi.ERR_WORKSPACE
 
 
 def test_binding_structs_match_the_header(tmp_path):

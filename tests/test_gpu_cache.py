@@ -474,3 +474,29 @@ def test_python_refusals():
         cache.plan(t, offs, total_tokens=2, slots=torch.empty(3, dtype=torch.int64, device=DEV))
     with pytest.raises(ValueError):
         cache.CacheTables(t.buf[:40], 1, 2, 3, 16)
+
+
+@pytest.mark.parametrize("H,d,ps,B,most,rows", [(40, 32, 16, 8, 2600, 1), (24, 64, 64, 13, 3000, 2),
+                                                (1, 128, 32, 2, 30000, 1), (40, 128, 64, 9, 2900, 1)])
+def test_long_histories(H, d, ps, B, most, rows):
+    """Blocks that walk many key tiles: more than their ring of stages, and more
+    than the page ids a warp holds at a time."""
+    g = np.random.default_rng(B)
+    lengths = g.integers(most // 2, most, size=B).tolist()
+    t, host = tables_of(lengths, ps, B)
+    pages = torch.full((t.num_pages, H, ps * (d + 8)), 255, dtype=torch.uint8, device=DEV)
+    tokens = []
+    slots = cache.slot_map(t, offs_of(lengths), total_tokens=sum(lengths))
+    gen = torch.Generator(device=DEV).manual_seed(B)
+    k, v = (torch.nn.functional.silu(torch.randn((sum(lengths), H, d), generator=gen, device=DEV))
+            .bfloat16() for _ in range(2))
+    cache.append(k, v, slots, pages, t)
+    at = 0
+    for n in lengths:
+        tokens.append(tuple((c.double(), s, m) for c, s, m in
+                            (ref.quantise(x[at:at + n].cpu()) for x in (k, v))))
+        at += n
+    for K1 in (1 << 20, 1100):
+        got, want, tol = run_attend(t, pages, tokens, lengths, [rows] * B, [0] * B, H, d, 3, K1=K1,
+                                    K2=100, ctx=0, max_new=rows)
+        check(got, want, tol)
