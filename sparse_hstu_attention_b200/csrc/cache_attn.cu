@@ -591,13 +591,19 @@ cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
 
 }  // namespace
 
+// Sequences of up to this many rows take the kernel above, longer ones tiles of
+// 128 rows on tcgen05.
+constexpr int kFewRows = 16;
+
 size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d) {
+  if (a.max_new > kFewRows) return cache_tc_ws_bytes(a, d);
   const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
   return p.S == 1 ? 256 : align256((size_t)p.units * p.S * kRows * d * sizeof(float));
 }
 
 cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st) {
   if (a.T == 0 || a.max_new == 0) return cudaSuccess;
+  if (a.max_new > kFewRows) return launch_cache_tc(a, d, ws, st);
   float* parts = static_cast<float*>(ws);
   if (d == 32) return launch_step<32>(a, parts, st);
   if (d == 64) return launch_step<64>(a, parts, st);

@@ -152,4 +152,8 @@ cudaError_t launch_cache_read(const CacheRowArgs& a, int d, cudaStream_t st);
 size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d);
 cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st);
 
+// Many rows per sequence (cache_attn_tc.cu).
+size_t cache_tc_ws_bytes(const CacheAttnArgs& a, int d);
+cudaError_t launch_cache_tc(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st);
+
 }  // namespace hstu

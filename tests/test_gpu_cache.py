@@ -477,7 +477,8 @@ def test_python_refusals():
 
 
 @pytest.mark.parametrize("H,d,ps,B,most,rows", [(40, 32, 16, 8, 2600, 1), (24, 64, 64, 13, 3000, 2),
-                                                (1, 128, 32, 2, 30000, 1), (40, 128, 64, 9, 2900, 1)])
+                                                (1, 128, 32, 2, 30000, 1), (40, 128, 64, 9, 2900, 1),
+                                              (80, 32, 32, 4, 6000, 1)])
 def test_long_histories(H, d, ps, B, most, rows):
     """Blocks that walk many key tiles: more than their ring of stages, and more
     than the page ids a warp holds at a time."""
@@ -496,7 +497,7 @@ def test_long_histories(H, d, ps, B, most, rows):
         tokens.append(tuple((c.double(), s, m) for c, s, m in
                             (ref.quantise(x[at:at + n].cpu()) for x in (k, v))))
         at += n
-    for K1 in (1 << 20, 1100):
+    for K1, bound in ((1 << 20, rows), (1100, rows), (1 << 20, 200)):  # 200: the kernel of many rows
         got, want, tol = run_attend(t, pages, tokens, lengths, [rows] * B, [0] * B, H, d, 3, K1=K1,
-                                    K2=100, ctx=0, max_new=rows)
+                                    K2=100, ctx=0, max_new=bound)
         check(got, want, tol)
