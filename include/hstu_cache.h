@@ -169,7 +169,8 @@ typedef struct {
 
 /* Workspace of a call with these sizes (the blocks' partial sums): 256-byte
  * aligned, contents need not be initialised; calls that may overlap need one
- * each.  0 on invalid arguments. */
+ * each.  0: the call needs none (NULL will do), or the arguments are invalid
+ * (the call itself says so). */
 size_t hstu_cache_attend_workspace_bytes(const hstu_cache_tables* t,
                                          const hstu_cache_attend_params* p);
 

@@ -49,23 +49,23 @@ class CacheTables:
     free_pages [num_pages], block_table [B, max_pages], each part starting at a
     multiple of 64 words."""
 
-    __slots__ = ("buf", "B", "max_pages", "num_pages", "page_size", "_c")
+    __slots__ = ("buf", "device", "B", "max_pages", "num_pages", "page_size", "_c")
 
     def __init__(self, buf: torch.Tensor, B: int, max_pages: int, num_pages: int,
                  page_size: int):
-        if buf.dtype != torch.int32 or not buf.is_cuda or not buf.is_contiguous():
+        if buf.dtype is not torch.int32 or not buf.is_cuda or not buf.is_contiguous():
             raise TypeError("buf must be a contiguous CUDA int32 tensor")
         if B < 1 or max_pages < 1 or num_pages < 1:
             raise ValueError("B, max_pages and num_pages must be at least 1")
-        if buf.numel() < self.words(B, max_pages, num_pages):
-            raise ValueError(f"buf has {buf.numel()} words, needs "
-                             f"{self.words(B, max_pages, num_pages)}")
-        self.buf, self.B, self.max_pages = buf, int(B), int(max_pages)
-        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        n = self.words(B, max_pages, num_pages)
+        if buf.numel() < n:
+            raise ValueError(f"buf has {buf.numel()} words, needs {n}")
+        self.buf, self.device = buf, buf.device
+        self.B, self.max_pages, self.num_pages, self.page_size = B, max_pages, num_pages, page_size
         p = buf.data_ptr()
-        free = p + 4 * (_HEADER + _pad(self.B))
-        self._c = _abi.CacheTablesC(self.B, self.max_pages, self.num_pages, self.page_size, p,
-                                    p + 64, p + 4 * _HEADER, free, free + 4 * _pad(self.num_pages))
+        free = p + 4 * (_HEADER + _pad(B))
+        self._c = _abi.CacheTablesC(B, max_pages, num_pages, page_size, p, p + 64,
+                                    p + 4 * _HEADER, free, free + 4 * _pad(num_pages))
 
     @staticmethod
     def words(B: int, max_pages: int, num_pages: int) -> int:
@@ -112,37 +112,28 @@ def allocate_pages(num_pages: int, H: int, d: int, page_size: int = 64,
     return torch.empty((num_pages, H, page_size * (d + 8)), dtype=torch.uint8, device=device)
 
 
-class _On:
-    """The library calls launch on the current device: make it the tensors'."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, device: torch.device):
-        same = device.index is None or device.index == torch.cuda.current_device()
-        self.guard = None if same else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
-
-
-def _check(code: int, where: str):
+def _launch(device: torch.device, stream, where: str, call, *args):
+    """call(*args, stream) with the tensors' device current (the library
+    launches there); raises on a status other than OK."""
+    i = device.index
+    if i == torch._C._cuda_getDevice():
+        code = call(*args, _stream(stream, i))
+    else:
+        with torch.cuda.device(device):
+            code = call(*args, _stream(stream, i))
     if code != _abi.OK:
         raise SLAError(code, where)
 
 
-def _stream(stream, device) -> int:
-    return int((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+def _stream(stream, index: int) -> int:
+    # torch.cuda.current_stream() builds a Stream object, 2 us a call
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _i32(t: Optional[torch.Tensor], n: int, name: str, device) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 tensor on {device}")
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
@@ -151,18 +142,19 @@ def _i32(t: Optional[torch.Tensor], n: int, name: str, device) -> Optional[int]:
 
 def _rows(t: torch.Tensor, name: str, T: int, H: int, d: int, device) -> int:
     """Checks a bf16 [T, H, d] tensor; returns its row stride."""
-    if t.dtype != torch.bfloat16 or t.device != device:
+    if t.dtype is not torch.bfloat16 or t.device != device:
         raise TypeError(f"{name} must be a bfloat16 tensor on {device}")
     if t.shape != (T, H, d):
         raise ValueError(f"{name} must be [{T}, {H}, {d}], got {tuple(t.shape)}")
-    if T > 0 and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+    row, head, dim = t.stride()
+    if T > 0 and (dim != 1 or (H > 1 and head != d)):
         raise ValueError(f"{name}: heads and head_dim must be dense (stride (*, {d}, 1))")
-    return t.stride(0) if T > 1 else H * d
+    return row if T > 1 else H * d
 
 
 def _pages(pages: torch.Tensor, tables: CacheTables):
     """(H, d, page stride in bytes) of a pages tensor."""
-    if pages.dtype != torch.uint8 or pages.device != tables.buf.device or pages.dim() != 3:
+    if pages.dtype is not torch.uint8 or pages.device != tables.device or pages.dim() != 3:
         raise TypeError("pages must be a uint8 tensor [num_pages, H, page_size * (d + 8)] on the "
                         "tables' device")
     P, H, n = pages.shape
@@ -171,9 +163,10 @@ def _pages(pages: torch.Tensor, tables: CacheTables):
     if P != tables.num_pages or H < 1 or d < 1 or n != ps * (d + 8):
         raise ValueError(f"pages must be [{tables.num_pages}, H, {ps} * (d + 8)], got "
                          f"{tuple(pages.shape)}")
-    if pages.stride(2) != 1 or (H > 1 and pages.stride(1) != n):
+    page, head, byte = pages.stride()
+    if byte != 1 or (H > 1 and head != n):
         raise ValueError("pages: the heads of a page must be dense")
-    return H, d, pages.stride(0) if P > 1 else H * n
+    return H, d, page if P > 1 else H * n
 
 
 def plan(tables: CacheTables, seq_offsets: torch.Tensor, num_targets: Optional[torch.Tensor] = None,
@@ -185,16 +178,15 @@ def plan(tables: CacheTables, seq_offsets: torch.Tensor, num_targets: Optional[t
     [total_tokens], -1 for candidates and for rows behind seq_offsets[B].
     seq_offsets: int32 [B + 1]; num_targets: int32 [B], the trailing candidates
     of each sequence; release: int32 [B], non-zero empties the slot first."""
-    dev = tables.buf.device
+    dev = tables.device
     o = _i32(seq_offsets, tables.B + 1, "seq_offsets", dev)
     nt = _i32(num_targets, tables.B, "num_targets", dev)
     rel = _i32(release, tables.B, "release", dev)
     slots = _slots_out(slots, total_tokens, dev)
     lib = _abi.load()
     ws = _workspace(workspace, lib.hstu_cache_plan_workspace_bytes(tables.B), dev, stream)
-    with _On(dev):
-        _check(lib.hstu_cache_plan(tables._c, o, nt, rel, total_tokens, slots.data_ptr(),
-                                   ws.data_ptr(), ws.numel(), _stream(stream, dev)), "hstu_cache_plan")
+    _launch(dev, stream, "hstu_cache_plan", lib.hstu_cache_plan, tables._c, o, nt, rel,
+            total_tokens, slots.data_ptr(), ws.data_ptr(), ws.numel())
     return slots
 
 
@@ -230,17 +222,16 @@ def slot_map(tables: CacheTables, seq_offsets: torch.Tensor, *, total_tokens: in
              slots: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Slots of the last seq_offsets[b + 1] - seq_offsets[b] cached tokens of
     every sequence (e.g. to read whole histories back)."""
-    dev = tables.buf.device
+    dev = tables.device
     o = _i32(seq_offsets, tables.B + 1, "seq_offsets", dev)
     slots = _slots_out(slots, total_tokens, dev)
-    with _On(dev):
-        _check(_abi.load().hstu_cache_slot_map(tables._c, o, total_tokens, slots.data_ptr(),
-                                               _stream(stream, dev)), "hstu_cache_slot_map")
+    _launch(dev, stream, "hstu_cache_slot_map", _abi.load().hstu_cache_slot_map, tables._c, o,
+            total_tokens, slots.data_ptr())
     return slots
 
 
 def _row_call(k, v, slots, pages, tables, H, d, page_stride):
-    dev = tables.buf.device
+    dev = tables.device
     T = slots.numel()
     return _abi.CacheRows(H, d, T, slots.data_ptr(), pages.data_ptr(), page_stride, k.data_ptr(),
                           v.data_ptr(), _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev))
@@ -251,12 +242,10 @@ def append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pages: torch.T
     """Quantise the rows of k and v ([T, H, d] bf16) into `pages` at `slots`
     (rows with a negative slot are skipped)."""
     H, d, stride = _pages(pages, tables)
-    dev = tables.buf.device
+    dev = tables.device
     _slots(slots, dev)
     r = _row_call(k, v, slots, pages, tables, H, d, stride)
-    with _On(dev):
-        _check(_abi.load().hstu_cache_append(tables._c, r, _stream(stream, dev)),
-               "hstu_cache_append")
+    _launch(dev, stream, "hstu_cache_append", _abi.load().hstu_cache_append, tables._c, r)
 
 
 def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
@@ -264,7 +253,7 @@ def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
     """The rows that `slots` hold, as bf16 (k, v) [T, H, d]; zeros for a
     negative slot."""
     H, d, stride = _pages(pages, tables)
-    dev = tables.buf.device
+    dev = tables.device
     _slots(slots, dev)
     T = slots.numel()
     if k is None:
@@ -272,9 +261,7 @@ def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
     if v is None:
         v = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
     r = _row_call(k, v, slots, pages, tables, H, d, stride)
-    with _On(dev):
-        _check(_abi.load().hstu_cache_read(tables._c, r, _stream(stream, dev)),
-               "hstu_cache_read")
+    _launch(dev, stream, "hstu_cache_read", _abi.load().hstu_cache_read, tables._c, r)
     return k, v
 
 
@@ -290,7 +277,7 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
     be None when num_targets is.  max_new: a bound on the rows of any sequence
     (default: all of them); a tight one gives a step of few rows its kernel."""
     H, d, stride = _pages(pages, tables)
-    dev = tables.buf.device
+    dev = tables.device
     T = q.shape[0]
     q_rs = _rows(q, "q", T, H, d, dev)
     k_ptr = v_ptr = None
@@ -309,15 +296,17 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
         float(alpha), float(N), q.data_ptr(), k_ptr, v_ptr, q_rs, k_rs, v_rs, pages.data_ptr(),
         stride, out.data_ptr(), _rows(out, "out", T, H, d, dev))
     lib = _abi.load()
-    ws = _workspace(workspace, lib.hstu_cache_attend_workspace_bytes(tables._c, p), dev, stream)
-    with _On(dev):
-        _check(lib.hstu_cache_attend(tables._c, p, ws.data_ptr(), ws.numel(),
-                                     _stream(stream, dev)), "hstu_cache_attend")
+    need = lib.hstu_cache_attend_workspace_bytes(tables._c, p)
+    ws = None
+    if need or workspace is not None:
+        ws = _workspace(workspace, need, dev, stream)
+    _launch(dev, stream, "hstu_cache_attend", lib.hstu_cache_attend, tables._c, p,
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out
 
 
 def get_error(tables: CacheTables, stream=None) -> int:
     """Synchronise and return the tables' status (0 = no error)."""
-    dev = tables.buf.device
-    with _On(dev):
-        return int(_abi.load().hstu_cache_get_error(tables._c, _stream(stream, dev)))
+    with torch.cuda.device(tables.device):
+        return int(_abi.load().hstu_cache_get_error(tables._c,
+                                                    _stream(stream, tables.device.index)))

@@ -183,8 +183,8 @@ int hstu_cache_attend(const hstu_cache_tables* t, const hstu_cache_attend_params
   CacheAttnArgs a;
   const int e = attend_args(t, p, &a);
   if (e) return e;
-  if (workspace == nullptr || !aligned(workspace, 256) ||
-      workspace_bytes < cache_attend_ws_bytes(a, p->d))
+  const size_t need = cache_attend_ws_bytes(a, p->d);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need))
     return HSTU_SLA_ERR_WORKSPACE;
   return status_of(
       launch_cache_attend(a, p->d, workspace, reinterpret_cast<cudaStream_t>(stream)));

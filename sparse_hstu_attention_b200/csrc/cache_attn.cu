@@ -598,7 +598,7 @@ constexpr int kFewRows = 16;
 size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d) {
   if (a.max_new > kFewRows) return cache_tc_ws_bytes(a, d);
   const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
-  return p.S == 1 ? 256 : align256((size_t)p.units * p.S * kRows * d * sizeof(float));
+  return p.S == 1 ? 0 : align256((size_t)p.units * p.S * kRows * d * sizeof(float));
 }
 
 cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st) {

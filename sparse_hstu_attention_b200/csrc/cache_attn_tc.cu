@@ -7,28 +7,34 @@
 //   out_i = (1/N) (sum_j (P_ij s'_j) c'_j + sum_j P_ij m'_j  [+ own pair]),
 // so what a masked place holds never enters a product: its P is selected to
 // zero, its codes are finite.  K codes are the f16 subnormals c 2^-24 and
-// 16 c 2^-24 there (q in f16, scaled by a power of two per row, its dims of the
-// high nibbles divided by 16); V codes are bf16 whole numbers, because P s' is
-// a bf16 operand: a row's P may span more than f16's range and the sums O stay
-// in TMEM, where rescaling them would cost a pass.  That rounding of P s' to
-// bf16 (2^-9 of itself) is the only one of more than 2^-12.
+// 16 c 2^-24 there; V codes are the bf16 numbers c / 64, because P s' is a bf16
+// operand: a row's P may span more than f16's range, and the sums O stay in
+// TMEM, where rescaling them would cost a pass.  That rounding of P s' to bf16
+// (2^-9 of itself) is the only one of more than 2^-12.  q enters as f16 times
+// 2^4, its dims of the high nibbles divided by 16: exact for rows whose largest
+// |q| lies in [2^-6, 2^11), down to 2^-12 of that largest; if a block has
+// another row, its rows are scaled by a power of two each, and the scores back.
 //
-// A block is one (sequence, head, 128 rows), 8 warps, and two blocks share an
-// SM: S = Q C^T (M = 128, N = 128 keys, K = d) and O += P C' (N = d, K = 128)
-// by tcgen05 into 128 + d TMEM columns, and all warps do the same things in
-// turn, so that one block's products run under the other's arithmetic:
+// A block is one (sequence, head, 128 rows), possibly a part of its keys, 8
+// warps, and two blocks share an SM: S = Q C^T (M = 128, N = 128 keys, K = d)
+// and O += P C' (N = d, K = 128) by tcgen05 into 128 + d TMEM columns.  All warps
+// do the same things in turn, and one block's products, loads and output run
+// under the other's arithmetic:
 //   V codes of tile n  -> shared memory     while S of tile n runs
 //   wait S; P = SiLU(x) masked, P s' -> TMEM over the scores; issue O += P C'
 //   K codes of tile n+1 -> shared memory    while that runs; issue S of n + 1
-// Codes come straight from the pages into registers, 16 bytes a thread, one
-// step before they are unpacked; the unpacked operands are K-major 128-byte
-// swizzled tiles (V transposed: its bytes lie along the tokens).  Scores are
-// read from TMEM as 16 x 256-bit fragments, so a thread has 4 rows and a quarter
-// of the columns and the per-key pairs are one 16-byte load per two columns and
-// four rows.
+// Codes come straight from the pages into registers, 16 bytes a thread, a tile
+// before they are unpacked; the unpacked operands are K-major 128-byte swizzled
+// tiles (V transposed: its bytes lie along the tokens).  Scores are read from
+// TMEM as 16 x 256-bit fragments: a thread has 4 rows and a quarter of the
+// columns, so the per-key pairs are one 16-byte load per two columns and four
+// rows.  The loops over 16-column pieces stay rolled: unrolled, the kernel's code
+// no longer fits the instruction cache, which cost more than the loops do.
 //
-// Bound: issue slots of the pointwise part (about 5 a score), then the tensor
-// cores and shared memory.
+// Bound: the special-function unit (one tanh a score, 1024 clocks a 128 x 128
+// tile and SM, as long as the tile's products take), then issue slots.
+#include <type_traits>
+
 #include "cache_common.cuh"
 #include "sm100.cuh"
 
@@ -39,7 +45,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 256, kBM = 128, kBN = 128;
-constexpr int kIdTiles = 32;  // tiles whose page ids are held at a time
+constexpr int kIdTiles = 32;  // tiles whose page blocks are held at a time
 constexpr uint32_t kColS = 0, kColO = 128, kTmemCols = 256;
 
 template <int D>
@@ -51,15 +57,15 @@ struct TcCfg {
   static constexpr int BOXV = D * 128;                 // D rows of 64 tokens
   static constexpr int OFF_Q = 0, OFF_K = TILE_K, OFF_V = 2 * TILE_K;
   static constexpr int OFF_PAR = OFF_V + 2 * BOXV;     // 2 x [64 column pairs][8] floats
-  static constexpr int OFF_F = OFF_PAR + 2 * 64 * 32;  // per row: factor, sum(q), own pair
-  static constexpr int OFF_REST = OFF_F + 3 * 128 * 4;  // [2][128]
-  static constexpr int OFF_IDS = OFF_REST + 2 * 128 * 4;  // [2][kIdTiles * 8] page ids
-  static constexpr int OFF_BAR = OFF_IDS + 2 * kIdTiles * 8 * 4;
+  static constexpr int OFF_ROW = OFF_PAR + 2 * 64 * 32;  // per row: factor, sum(q), own pair
+  static constexpr int OFF_REST = OFF_ROW + 3 * 128 * 4;  // [2][128]
+  static constexpr int OFF_IDS = OFF_REST + 2 * 128 * 4;  // [2][kIdTiles * 8] page blocks
+  static constexpr int OFF_BAR = OFF_IDS + 2 * kIdTiles * 8 * 8;
   static constexpr int NEED = OFF_BAR + 32 + 1024;     // + alignment slack
   // two blocks an SM, no more: their TMEM columns are all there are
   static constexpr int SMEM = NEED > 80 * 1024 ? NEED : 80 * 1024;
+  static_assert(SMEM <= 113 * 1024, "two blocks an SM");
   static constexpr uint32_t SWZK = SWK == 128 ? kSwizzle128B : kSwizzle64B;
-  static constexpr int CHK = D / 32;                   // 16-byte chunks of a K code row, per lane group
 };
 
 // kind::f16 with f16 A / B (format 0) and f32 accumulator, both K-major.
@@ -67,23 +73,29 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 16 lanes x 32 columns: regs 4i .. 4i + 3 are row g, columns 8i + 2t, + 1, and
+// 16 lanes x 16 columns: regs 4i .. 4i + 3 are row g, columns 8i + 2t, + 1, and
 // row g + 8, the same columns.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15}, [%16];"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+        "=r"(r[7])
       : "r"(taddr));
 }
-// 16 lanes x 16 columns: regs 2i, 2i + 1 are rows g and g + 8, column 4i + t.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
+// Waits for two of them.
+__device__ __forceinline__ void tmem_ld_frag_wait(uint32_t (&r)[8], uint32_t (&s)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(s[0]), "+r"(s[1]), "+r"(s[2]), "+r"(s[3]),
+                 "+r"(s[4]), "+r"(s[5]), "+r"(s[6]), "+r"(s[7])
+               :
+               : "memory");
+}
+// 16 lanes x 8 columns: regs 2i, 2i + 1 are rows g and g + 8, column 4i + t.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -93,17 +105,31 @@ __device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t sub16_bf16x2(uint32_t x) {  // 16 + c -> c, exact
+// Codes in bits 0..3 of the halves, the bf16 subnormals c 2^-133, times 2^127:
+// the bf16 numbers c / 64, exact.
+__device__ __forceinline__ uint32_t code_bf16x2(uint32_t x) {
   uint32_t r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0xc180c180u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x & 0x000f000fu), "r"(0x7f007f00u));
   return r;
 }
 
-// Bounded wait for the phase of parity `parity`: false after kWaitLimitNs.
+// Bounded wait for the phase of parity `parity`: false after kWaitLimitNs.  A
+// try may sleep for up to 10 us, so that waiting warps leave the issue slots to
+// the others.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(10000u)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool phase_wait(uint32_t bar, uint32_t parity, const CacheTab& t) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (try_wait_long(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!try_wait_long(bar, parity)) {
     if (globaltimer() - t0 > kWaitLimitNs) {
       cache_fail(t, HSTU_SLA_ERR_TIMEOUT);
       return false;
@@ -140,11 +166,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t sQ = base + C::OFF_Q, sK = base + C::OFF_K, sV = base + C::OFF_V;
   const uint32_t bar_s = base + C::OFF_BAR, bar_o = bar_s + 8;
   uint32_t* const slot = reinterpret_cast<uint32_t*>(sm + C::OFF_BAR + 16);
-  float* const row_f = reinterpret_cast<float*>(sm + C::OFF_F);
-  float* const row_sum = row_f + 128;
-  float* const row_self = row_f + 256;
+  float* const rd = reinterpret_cast<float*>(sm + C::OFF_ROW);
   float* const rests = reinterpret_cast<float*>(sm + C::OFF_REST);
-  int* const ids = reinterpret_cast<int*>(sm + C::OFF_IDS);
+  const uint8_t** const blocks = reinterpret_cast<const uint8_t**>(sm + C::OFF_IDS);
 
   if (warp == 0) {
     tmem_alloc(smem_addr(slot), kTmemCols);
@@ -162,27 +186,27 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int32_t* const bt = a.t.bt + (int64_t)b * a.t.M;
   const uint8_t* const head = a.pages + (int64_t)h * lay.bytes;
 
-  // Page ids of the tiles [32 c, 32 c + 32): -1 past the cached tokens.
+  // This head's block of the pages of tiles [32 c, 32 c + 32): null past the
+  // cached tokens.
   auto load_ids = [&](int c) {
     const int n = c * kIdTiles + (tid >> lpt);
     if (tid >= kIdTiles << lpt) return;
-    int id = -1;
+    const uint8_t* p = nullptr;
     if (n < nt) {
       const int i = (tl.at(e0 + n) << lpt) + (tid & ((1 << lpt) - 1));
       if (i < pages) {
-        id = bt[i];
-        if (id < 0 || id >= a.t.P) {
+        const int id = bt[i];
+        if (id >= 0 && id < a.t.P)
+          p = head + id * a.page_stride;
+        else
           cache_fail(a.t, HSTU_SLA_ERR_BAD_INPUT);
-          id = -1;
-        }
       }
     }
-    ids[(c & 1) * (kIdTiles * 8) + tid] = id;
+    blocks[(c & 1) * (kIdTiles * 8) + tid] = p;
   };
-  // Block of the page that holds token `tok` of tile n, or null.
-  auto page_of = [&](int n, int tok) -> const uint8_t* {
-    const int id = ids[((n / kIdTiles) & 1) * (kIdTiles * 8) + ((n % kIdTiles) << lpt) + (tok >> lps)];
-    return id < 0 ? nullptr : head + id * a.page_stride;
+  // Table entry of the first page of tile n.
+  auto entry = [&](int n) -> const uint8_t* const* {
+    return blocks + ((n / kIdTiles) & 1) * (kIdTiles * 8) + ((n % kIdTiles) << lpt);
   };
   load_ids(0);
   tc_fence_before();
@@ -190,169 +214,200 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *slot;
 
-  // K codes: lane takes token 8 (..) + lane % 8 and D / 8 of its bytes.
+  const float fac = 0.5f * a.alpha * 1048576.f;  // codes 2^-24, q 2^4
+  // K codes: lane takes token 8 (..) + lane % 8 and D / 8 of its bytes, of the
+  // tile's first 64 tokens and of the others (the same place, other pages).
   uint32_t kc[2][4], vc[2][4], kpar = 0, vpar = 0;
+  const int ktok = warp * 8 + (lane & 7), kq = lane >> 3;
+  const int k_page = ktok >> lps, k_off = (ktok & (ps - 1)) * (D / 2) + kq * (D / 8);
+  const int par_page = tid >> lps, par_off = lay.kp + 4 * (tid & (ps - 1));
   auto load_k = [&](int n) {
+    const uint8_t* const* e = entry(n);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int tok = x * 64 + warp * 8 + (lane & 7);
-      const uint8_t* p = page_of(n, tok);
+      const uint8_t* p = e[k_page + (x ? 64 >> lps : 0)];
 #pragma unroll
       for (int w = 0; w < 4; ++w) kc[x][w] = 0;
       if (p) {
-        p += (tok & (ps - 1)) * (D / 2) + (lane >> 3) * (D / 8);
         if constexpr (D == 128) {
-          const uint4 y = *reinterpret_cast<const uint4*>(p);
+          const uint4 y = *reinterpret_cast<const uint4*>(p + k_off);
           kc[x][0] = y.x; kc[x][1] = y.y; kc[x][2] = y.z; kc[x][3] = y.w;
         } else if constexpr (D == 64) {
-          const uint2 y = *reinterpret_cast<const uint2*>(p);
+          const uint2 y = *reinterpret_cast<const uint2*>(p + k_off);
           kc[x][0] = y.x; kc[x][1] = y.y;
         } else {
-          kc[x][0] = *reinterpret_cast<const uint32_t*>(p);
+          kc[x][0] = *reinterpret_cast<const uint32_t*>(p + k_off);
         }
       }
     }
     kpar = vpar = 0;
     if (tid < kBN) {
-      const uint8_t* p = page_of(n, tid);
+      const uint8_t* p = e[par_page];
       if (p) {
-        kpar = *reinterpret_cast<const uint32_t*>(p + lay.kp + 4 * (tid & (ps - 1)));
-        vpar = *reinterpret_cast<const uint32_t*>(p + lay.vp + 4 * (tid & (ps - 1)));
+        kpar = *reinterpret_cast<const uint32_t*>(p + par_off);
+        vpar = *reinterpret_cast<const uint32_t*>(p + par_off + 4 * ps);
       }
     }
   };
   // f16 codes into the K tile; the pairs of token tid as floats, column pairs
   // together: s s m m, s' s' m' m'.
+  uint32_t k_at;  // where the lane's first 16 bytes go (the next: xor 16, 32, 48)
+  {
+    const int byte = kq * (D / 2);  // of the token's f16 row
+    const uint32_t sw = C::SWK == 128 ? (uint32_t)(ktok & 7) : (uint32_t)((ktok >> 1) & 3);
+    k_at = sK + byte / C::SWK * C::BOXK + ktok * C::SWK + ((((byte % C::SWK) >> 4) ^ sw) << 4);
+  }
+  const uint32_t par_at = (uint32_t)(tid >> 1) * 32 + (tid & 1) * 4;
   auto store_k = [&](int n) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int tok = x * 64 + warp * 8 + (lane & 7);
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
-        const int byte = (lane >> 3) * (D / 2) + w * 16;  // of the token's f16 row
-        const uint32_t c = (byte % C::SWK) >> 4;
-        const uint32_t sw = C::SWK == 128 ? (uint32_t)(tok & 7) : (uint32_t)((tok >> 1) & 3);
         const uint32_t y = kc[x][w], z = y >> 8;
-        st_shared_v4(sK + byte / C::SWK * C::BOXK + tok * C::SWK + ((c ^ sw) << 4),
-                     y & 0x000f000fu, y & 0x00f000f0u, z & 0x000f000fu, z & 0x00f000f0u);
+        st_shared_v4((k_at ^ (w << 4)) + x * 64 * C::SWK, y & 0x000f000fu, y & 0x00f000f0u,
+                     z & 0x000f000fu, z & 0x00f000f0u);
       }
-    }
     if (tid < kBN) {
-      float* p = reinterpret_cast<float*>(sm + C::OFF_PAR + (n & 1) * 2048) + (tid >> 1) * 8 +
-                 (tid & 1);
-      p[0] = bf_lo(kpar);
+      float* p = reinterpret_cast<float*>(sm + C::OFF_PAR + (n & 1) * 2048 + par_at);
+      p[0] = bf_lo(kpar) * fac;
       p[2] = bf_hi(kpar);
-      p[4] = bf_lo(vpar);
+      p[4] = bf_lo(vpar) * 64.f;
       p[6] = bf_hi(vpar);
     }
   };
-  // V codes: lane takes dim pair i and 16 tokens, in each half of the tile.
-  constexpr int VI = D / 2 / 8;  // warps a half of the tile needs
+  // V codes: lane takes a dim pair and 16 tokens: D / 16 warps cover 64 tokens,
+  // so at d = 128 a warp has its place in either half of the tile, and at less
+  // the first D / 8 warps have one.
+  constexpr int VI = D / 16, VX = D == 128 ? 2 : 1;
+  const bool v_warp = D == 128 || warp < 2 * VI;
+  const int v_half = D == 128 ? 0 : warp / VI, v_i = (warp % VI) * 8 + (lane & 7);
+  const int v_tok = v_half * 64 + 16 * (lane >> 3);
+  const int v_page = v_tok >> lps, v_off = lay.v + v_i * ps + (v_tok & (ps - 1));
   auto load_v = [&](int n) {
+    const uint8_t* const* e = entry(n);
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int job = x * 8 + warp, half = job / VI, i = (job % VI) * 8 + (lane & 7);
-      const int tok = half * 64 + 16 * (lane >> 3);
+    for (int x = 0; x < VX; ++x) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) vc[x][w] = 0;
-      if (half < 2) {
-        const uint8_t* p = page_of(n, tok);
-        if (p) {
-          const uint4 y = *reinterpret_cast<const uint4*>(p + lay.v + i * ps + (tok & (ps - 1)));
-          vc[x][0] = y.x; vc[x][1] = y.y; vc[x][2] = y.z; vc[x][3] = y.w;
-        }
+      const uint8_t* p = v_warp ? e[v_page + (x ? 64 >> lps : 0)] : nullptr;
+      if (p) {
+        const uint4 y = *reinterpret_cast<const uint4*>(p + v_off);
+        vc[x][0] = y.x; vc[x][1] = y.y; vc[x][2] = y.z; vc[x][3] = y.w;
       }
     }
   };
-  // bf16 codes into the V tile, rows = dims.  Lanes 0-3 of eight store the even
+  // bf16 codes / 64 into the V tile, rows = dims.  Lanes 0-3 of eight store the even
   // dim first and lanes 4-7 the odd one, which keeps the eight in eight
   // different 16-byte columns of the swizzle.
+  const uint32_t v_odd = (lane >> 2) & 1;
+  const uint32_t v_row = 2 * v_i + v_odd;
+  const uint32_t v_at = sV + v_half * C::BOXV + v_row * 128 + (((2 * (lane >> 3)) ^ (v_row & 7)) << 4);
+  const uint32_t v_sh = 4 * v_odd;
   auto store_v = [&]() {
+    if (!v_warp) return;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int job = x * 8 + warp, half = job / VI, i = (job % VI) * 8 + (lane & 7);
-      if (half < 2) {
+    for (int x = 0; x < VX; ++x)
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-          const int odd = pass ^ ((lane >> 2) & 1), row = 2 * i + odd;
-          const uint32_t at = sV + half * C::BOXV + row * 128;
-          const uint32_t sh = (4 * odd + 29) & 31;  // nibble to bits 3..6: right by 4 odd - 3
-          uint32_t r[8];
+      for (int pass = 0; pass < 2; ++pass) {
+        // the other dim of the pair: row ^ 1, and so its chunks' places ^ 1
+        const uint32_t at = (pass ? v_at ^ 144u : v_at) + x * C::BOXV;
+        const uint32_t sh = pass ? v_sh ^ 4u : v_sh;
+        uint32_t r[8];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t y = __funnelshift_r(vc[x][w], vc[x][w], sh);
-            const uint32_t z = __funnelshift_r(vc[x][w], vc[x][w], (sh + 8) & 31);
-            r[2 * w] = sub16_bf16x2((y & 0x00780078u) | 0x41804180u);
-            r[2 * w + 1] = sub16_bf16x2((z & 0x00780078u) | 0x41804180u);
-          }
-          const uint32_t c = 2 * (lane >> 3);
-          st_shared_v4(at + ((c ^ (row & 7)) << 4), r[0], r[1], r[2], r[3]);
-          st_shared_v4(at + (((c + 1) ^ (row & 7)) << 4), r[4], r[5], r[6], r[7]);
+        for (int w = 0; w < 4; ++w) {
+          r[2 * w] = code_bf16x2(vc[x][w] >> sh);
+          r[2 * w + 1] = code_bf16x2(vc[x][w] >> (sh + 8));
         }
+        st_shared_v4(at, r[0], r[1], r[2], r[3]);
+        st_shared_v4(at ^ 16u, r[4], r[5], r[6], r[7]);
       }
-    }
   };
 
   if (nt > 0) {
     load_k(0);
     load_v(0);
   }
-  // Q: two threads a row, half of its dims each.
+  // q into shared memory: D / 8 lanes a row, 16 rows a warp.
+  bool common;
   {
-    const int r = tid >> 1, half = tid & 1;
-    constexpr int W = D / 4;  // words of a half row
-    uint32_t x[W];
-    float sum = 0.f, own = 0.f;
-    uint32_t most = 0;
-    const int64_t row = sq.s0 + r0 + r;
-#pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      uint4 y = make_uint4(0, 0, 0, 0);
-      if (r < nr)
-        y = *reinterpret_cast<const uint4*>(a.q + row * a.q_rs + h * D + half * (D / 2) + 2 * i);
-      x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
-    }
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      sum += bf_lo(x[i]) + bf_hi(x[i]);
-      most = umax(most, umax(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
-    }
-    if (r < nr && r0 + r >= sq.h) {
-#pragma unroll
-      for (int i = 0; i < W; i += 4) {
-        const uint4 y =
-            *reinterpret_cast<const uint4*>(a.k + row * a.k_rs + h * D + half * (D / 2) + 2 * i);
-        own = fmaf(bf_lo(x[i]), bf_lo(y.x), fmaf(bf_hi(x[i]), bf_hi(y.x), own));
-        own = fmaf(bf_lo(x[i + 1]), bf_lo(y.y), fmaf(bf_hi(x[i + 1]), bf_hi(y.y), own));
-        own = fmaf(bf_lo(x[i + 2]), bf_lo(y.z), fmaf(bf_hi(x[i + 2]), bf_hi(y.z), own));
-        own = fmaf(bf_lo(x[i + 3]), bf_lo(y.w), fmaf(bf_hi(x[i + 3]), bf_hi(y.w), own));
-      }
-    }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    own += __shfl_xor_sync(0xffffffffu, own, 1);
-    most = umax(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    // as in cache_attn.cu: the row's largest |q| to [2^14, 2^15)
-    const int e = imax((int)(most >> 7) - 127, -112);
-    const float up = __int_as_float((141 - e) << 23), down = __int_as_float((113 + e) << 23);
-    if (half == 0) {
-      row_f[r] = down * (0.5f * a.alpha * 16777216.f);
-      row_sum[r] = most >= 0x7f80u ? __int_as_float(0x7fc00000) : sum * (0.5f * a.alpha);
-      const float z = own * a.alpha;
-      row_self[r] = r < nr && r0 + r >= sq.h ? z / (1.f + __expf(-z)) : 0.f;
-    }
-    const uint32_t sw = C::SWK == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
-#pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      const int byte = half * D + 4 * i;
-      uint32_t y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float z = j & 1 ? up * 0.0625f : up;
-        y[j] = pack_f16x2(bf_lo(x[i + j]) * z, bf_hi(x[i + j]) * z);
-      }
+    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI, UB = IT < 4 ? IT : 4;
+    const int ch = lane % LPR, rw = warp * 16 + lane / LPR;
+    const bf16* qp = a.q + (int64_t)(sq.s0 + r0 + rw) * a.q_rs + h * D + ch * 8;
+    const bf16* kp = a.k + (int64_t)(sq.s0 + r0 + rw) * a.k_rs + h * D + ch * 8;
+    const int cand = sq.h - r0;  // first candidate row of the block
+    // 16 bytes of f16 (q times up; the dims of high nibbles over 16) into row r
+    auto put = [&](int r, const uint4& y, float up) {
+      const uint32_t sw = C::SWK == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
+      const int byte = 16 * ch;
+      const float hi = up * 0.0625f;
       st_shared_v4(sQ + byte / C::SWK * C::BOXK + r * C::SWK +
                        ((((uint32_t)(byte % C::SWK) >> 4) ^ sw) << 4),
-                   y[0], y[1], y[2], y[3]);
+                   pack_f16x2(bf_lo(y.x) * up, bf_hi(y.x) * up),
+                   pack_f16x2(bf_lo(y.y) * hi, bf_hi(y.y) * hi),
+                   pack_f16x2(bf_lo(y.z) * up, bf_hi(y.z) * up),
+                   pack_f16x2(bf_lo(y.w) * hi, bf_hi(y.w) * hi));
+    };
+    bool fits = true;
+#pragma unroll 1
+    for (int i0 = 0; i0 < IT; i0 += UB) {
+      uint4 q[UB], k[UB];  // (all loads before the first use)
+#pragma unroll
+      for (int i = 0; i < UB; ++i) {
+        const int r = rw + (i0 + i) * RPI;
+        q[i] = k[i] = make_uint4(0, 0, 0, 0);
+        if (r < nr) q[i] = *reinterpret_cast<const uint4*>(qp + (int64_t)(i0 + i) * RPI * a.q_rs);
+        if (r < nr && r >= cand)
+          k[i] = *reinterpret_cast<const uint4*>(kp + (int64_t)(i0 + i) * RPI * a.k_rs);
+      }
+      float sum[UB], own[UB];
+      uint32_t most[UB];
+#pragma unroll
+      for (int i = 0; i < UB; ++i) {
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+        const uint32_t z[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
+        sum[i] = own[i] = 0.f;
+        most[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[i] += bf_lo(w[j]) + bf_hi(w[j]);
+          own[i] = fmaf(bf_lo(w[j]), bf_lo(z[j]), fmaf(bf_hi(w[j]), bf_hi(z[j]), own[i]));
+          most[i] = umax(most[i], umax(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+        }
+        put(rw + (i0 + i) * RPI, q[i], 16.f);
+      }
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < UB; ++i) {
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+          own[i] += __shfl_xor_sync(0xffffffffu, own[i], o);
+          most[i] = umax(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
+        }
+#pragma unroll
+      for (int i = 0; i < UB; ++i) {
+        const int r = rw + (i0 + i) * RPI;
+        // most in [2^-6, 2^11), or a row of zeros: 2^4 will do; else the row's
+        // largest goes to [2^14, 2^15) (values below 2^-112: times 2^126)
+        fits = fits && (most[i] == 0 || (most[i] >= 121u << 7 && most[i] < 138u << 7));
+        if (ch == 0) {
+          const int e = imax((int)(most[i] >> 7) - 127, -112);
+          rd[r] = __int_as_float(imin(117 + e, 254) << 23);  // 2^(e - 10)
+          rd[128 + r] =
+              most[i] >= 0x7f80u ? __int_as_float(0x7fc00000) : sum[i] * (0.5f * a.alpha);
+          const float y = own[i] * a.alpha;
+          rd[256 + r] = r >= cand ? __fdividef(y, 1.f + __expf(-y)) : 0.f;
+        }
+      }
+    }
+    common = __syncthreads_and(fits);
+    if (!common) {  // 2^(14 - e) for each row
+#pragma unroll 1
+      for (int i = 0; i < IT; ++i) {
+        const int r = rw + i * RPI;
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (r < nr) q = *reinterpret_cast<const uint4*>(qp + (int64_t)i * RPI * a.q_rs);
+        put(r, q, 16.f / rd[r]);
+      }
     }
   }
 
@@ -400,10 +455,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_before();
     __syncthreads();
     if (warp == 0) issue_s();
-    const float f[4] = {row_f[quad * 32 + g], row_f[quad * 32 + g + 8], row_f[quad * 32 + g + 16],
-                        row_f[quad * 32 + g + 24]};
-    const float qs[4] = {row_sum[quad * 32 + g], row_sum[quad * 32 + g + 8],
-                         row_sum[quad * 32 + g + 16], row_sum[quad * 32 + g + 24]};
+    const uint64_t qs[4] = {f2s(rd[128 + quad * 32 + g]), f2s(rd[128 + quad * 32 + g + 8]),
+                            f2s(rd[128 + quad * 32 + g + 16]),
+                            f2s(rd[128 + quad * 32 + g + 24])};
     int n = 0;
     for (; n < nt; ++n) {
       // V of this tile, once the last tile's product has read its own
@@ -411,7 +465,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (ok) {
         store_v();
         fence_proxy_async_smem();
-        if (n + 1 < nt) load_k(n + 1);
+        if (n + 1 < nt) {
+          load_k(n + 1);
+          load_v(n + 1);
+        }
         if ((n & (kIdTiles - 1)) == 8 && n + kIdTiles - 8 < nt) load_ids(n / kIdTiles + 1);
         ok = phase_wait(bar_s, n & 1, a.t);
       }
@@ -421,63 +478,72 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       tc_fence_after();
       const int j0 = tl.at(e0 + n) * kBN;
-      const bool full = whole(j0, kBN);
-      const float4* par =
-          reinterpret_cast<const float4*>(sm + C::OFF_PAR + (n & 1) * 2048) + chalf * 64;
+      const ulonglong2* par =
+          reinterpret_cast<const ulonglong2*>(sm + C::OFF_PAR + (n & 1) * 2048) + chalf * 64;
+      // FAST: every pair visible, one factor for all rows (in the steps s)
+      auto pointwise = [&](auto fast) {
+        constexpr bool FAST = decltype(fast)::value;
+#pragma unroll 1
+        for (int cg = 0; cg < 4; ++cg) {  // 16 columns each
+          const uint32_t at = lanes + kColS + chalf * 64 + cg * 16;
+          uint32_t s0[8], s1[8];
+          tmem_ld_frag(at, s0);
+          tmem_ld_frag(at + (16u << 16), s1);
+          tmem_ld_frag_wait(s0, s1);
+          uint32_t bits[4];
+          float f[4];
+          if constexpr (!FAST) {
+            // this thread's columns of the 16, per row
+            const int jc = j0 + chalf * 64 + cg * 16;
 #pragma unroll
-      for (int cg = 0; cg < 2; ++cg) {  // 32 columns each
-        const uint32_t at = lanes + kColS + chalf * 64 + cg * 32;
-        uint32_t s0[16], s1[16];
-        tmem_ld_frag(at, s0);
-        tmem_ld_frag(at + (16u << 16), s1);
-        tmem_ld_wait2(s0, s1);
-        uint32_t bits[4] = {0, 0, 0, 0};
-        if (!full) {
-          // this thread's columns of the 32, per row
-          const int jc = j0 + chalf * 64 + cg * 32;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const CacheRow c = cache_row(r0 + imin(quad * 32 + g + 8 * i, nr - 1), sq.h, sq.Lh,
-                                         a.K1, a.K2e);
-            bits[i] = (range_bits(0, c.pre, jc) | range_bits(c.lo, c.hi, jc)) >> (2 * t);
-          }
-        }
-        uint32_t p0[8], p1[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // 8 columns each
-          const float4 kp = par[(cg * 16 + 4 * i + t) * 2];      // s s m m
-          const float4 vp = par[(cg * 16 + 4 * i + t) * 2 + 1];  // of V
-          const uint64_t ks = f2(__float_as_uint(kp.x), __float_as_uint(kp.y));
-          const uint64_t km = f2(__float_as_uint(kp.z), __float_as_uint(kp.w));
-          const uint64_t vs = f2(__float_as_uint(vp.x), __float_as_uint(vp.y));
-          const uint64_t vm = f2(__float_as_uint(vp.z), __float_as_uint(vp.w));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t* s = (r < 2 ? s0 : s1) + 4 * i + 2 * (r & 1);
-            const uint64_t x =
-                f2_fma(f2_mul(f2(s[0], s[1]), f2s(f[r])), ks, f2_mul(km, f2s(qs[r])));
-            const uint64_t p = f2_fma(x, f2_tanh(x), x);
-            uint64_t pm = f2_mul(p, vm);
-            uint32_t pv = f2_bf16(f2_mul(p, vs));
-            if (!full) {
-              const bool a0 = bits[r] >> (8 * i) & 1u, a1 = bits[r] >> (8 * i + 1) & 1u;
-              pv &= (a0 ? 0xffffu : 0u) | (a1 ? 0xffff0000u : 0u);
-              pm = f2(a0 ? (uint32_t)pm : 0u, a1 ? (uint32_t)(pm >> 32) : 0u);
+            for (int i = 0; i < 4; ++i) {
+              const CacheRow c = cache_row(r0 + imin(quad * 32 + g + 8 * i, nr - 1), sq.h,
+                                           sq.Lh, a.K1, a.K2e);
+              bits[i] = (range_bits(0, c.pre, jc) | range_bits(c.lo, c.hi, jc)) >> (2 * t);
+              f[i] = common ? 1.f : rd[quad * 32 + g + 8 * i];
             }
-            rest[r] = f2_add(rest[r], pm);
-            (r < 2 ? p0 : p1)[2 * i + (r & 1)] = pv;
           }
+          uint32_t p0[4], p1[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {  // 8 columns each
+            const ulonglong2 kp = par[(cg * 8 + 4 * i + t) * 2];      // s s, m m
+            const ulonglong2 vp = par[(cg * 8 + 4 * i + t) * 2 + 1];  // of V
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t* s = (r < 2 ? s0 : s1) + 4 * i + 2 * (r & 1);
+              uint64_t y = f2(s[0], s[1]);
+              if constexpr (!FAST) y = f2_mul(y, f2s(f[r]));
+              y = f2_fma(y, kp.x, f2_mul(kp.y, qs[r]));
+              const uint64_t p = f2_fma(y, f2_tanh(y), y);
+              uint32_t pv = f2_bf16(f2_mul(p, vp.x));
+              if constexpr (FAST) {
+                rest[r] = f2_fma(p, vp.y, rest[r]);
+              } else {
+                const bool a0 = bits[r] >> (8 * i) & 1u, a1 = bits[r] >> (8 * i + 1) & 1u;
+                pv &= (a0 ? 0xffffu : 0u) | (a1 ? 0xffff0000u : 0u);
+                const uint64_t pm = f2_mul(p, vp.y);
+                rest[r] = f2_add(rest[r], f2(a0 ? (uint32_t)pm : 0u,
+                                             a1 ? (uint32_t)(pm >> 32) : 0u));
+              }
+              (r < 2 ? p0 : p1)[2 * i + (r & 1)] = pv;
+            }
+          }
+          // P of columns [32 c, 32 c + 32) in columns [32 c, 32 c + 16)
+          const uint32_t to = lanes + kColS + chalf * 64 + (cg >> 1) * 32 + (cg & 1) * 8;
+          tmem_st_frag(to, p0);
+          tmem_st_frag(to + (16u << 16), p1);
         }
-        tmem_st_frag(at, p0);
-        tmem_st_frag(at + (16u << 16), p1);
-      }
+      };
+      if (common && whole(j0, kBN))
+        pointwise(std::true_type{});
+      else
+        pointwise(std::false_type{});
       tmem_st_wait();
       tc_fence_before();
       __syncthreads();
       if (warp == 0) issue_o(n == 0);
       if (n + 1 < nt) {
         store_k(n + 1);
-        load_v(n + 1);
         fence_proxy_async_smem();
         __syncthreads();
         if (warp == 0) issue_s();
@@ -503,52 +569,89 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
 
-  // Epilogue: lane = row, each column half by its warps, 16 dims at a time.
+  // Out: O as 16 x 256-bit fragments, turned among the four lanes of a row so that
+  // each has 8 dims in a row (16 bytes of bf16; 64 bytes a row and 8 rows an
+  // instruction).  A warp has its quarter's rows and half of the dims, at d = 32
+  // half of the rows.
   {
-    const int r = quad * 32 + lane;
-    const float rs = rests[r] + rests[128 + r], own = row_self[r];
-    const int64_t row = sq.s0 + r0 + r;
-    constexpr int CW = D / 2;  // dims of this warp
+    constexpr int NA = D >= 64 ? 2 : 1, NC = D == 128 ? 2 : 1;
+    const int64_t row0 = sq.s0 + r0;
+    const int cand = sq.h - r0;  // first candidate row
+#pragma unroll 1
+    for (int ac = 0; ac < NA * NC; ++ac) {
+      const int la = D >= 64 ? ac / NC : chalf;                 // 16 lanes of the quarter
+      const int c0 = D >= 64 ? (chalf * NC + ac % NC) * 32 : 0;  // 32 dims
+      uint4 vv[2];  // the candidates' v
 #pragma unroll
-    for (int c = 0; c < CW; c += 16) {
-      const int d0 = chalf * CW + c;
-      uint32_t o[16];
+      for (int hr = 0; hr < 2; ++hr) {
+        const int r = quad * 32 + 16 * la + 8 * hr + g;
+        vv[hr] = make_uint4(0, 0, 0, 0);
+        if (S == 1 && r >= cand && r < nr)
+          vv[hr] = *reinterpret_cast<const uint4*>(a.v + (row0 + r) * a.v_rs + h * D +
+                                                   c0 + 8 * t);
+      }
+      uint32_t oa[8], ob[8];
       if (nt > 0) {
-        tmem_ld16(lanes + kColO + d0, o);
-        tmem_ld_wait(o);
+        const uint32_t at = lanes + ((uint32_t)(16 * la) << 16) + kColO + c0;
+        tmem_ld_frag(at, oa);
+        tmem_ld_frag(at + 16, ob);
+        tmem_ld_frag_wait(oa, ob);
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = 0;
+        for (int i = 0; i < 8; ++i) oa[i] = ob[i] = 0;
       }
-      if (r < nr && S > 1) {
-        float4* dst = reinterpret_cast<float4*>(parts + ((int64_t)blockIdx.x * kBM + r) * D + d0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_float4(__uint_as_float(o[4 * i]) + rs, __uint_as_float(o[4 * i + 1]) + rs,
-                               __uint_as_float(o[4 * i + 2]) + rs,
-                               __uint_as_float(o[4 * i + 3]) + rs);
-      } else if (r < nr) {
-        uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        const bool is_cand = r0 + r >= sq.h;
-        if (is_cand) {
-          const uint4* vp = reinterpret_cast<const uint4*>(a.v + row * a.v_rs + h * D + d0);
-          const uint4 y = vp[0], z = vp[1];
-          v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
-          v[4] = z.x; v[5] = z.y; v[6] = z.z; v[7] = z.w;
+      for (int hr = 0; hr < 2; ++hr) {
+        // y[2 i], y[2 i + 1]: dims 8 i + 2 t, + 1 -> after the turn 8 t + 2 i, + 1
+        uint32_t y[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          y[2 * i] = oa[4 * i + 2 * hr];
+          y[2 * i + 1] = oa[4 * i + 2 * hr + 1];
+          y[4 + 2 * i] = ob[4 * i + 2 * hr];
+          y[5 + 2 * i] = ob[4 * i + 2 * hr + 1];
         }
-        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float x = __uint_as_float(o[2 * i]) + rs, y = __uint_as_float(o[2 * i + 1]) + rs;
-          if (is_cand) {
-            x = fmaf(own, bf_lo(v[i]), x);
-            y = fmaf(own, bf_hi(v[i]), y);
+        for (int st = 1; st < 4; st <<= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i & st) continue;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              uint32_t& lo = y[2 * i + z];
+              uint32_t& hi = y[2 * (i + st) + z];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, t & st ? lo : hi, st);
+              if (t & st) lo = got; else hi = got;
+            }
           }
-          w[i] = pack_bf16x2(x * a.inv_n, y * a.inv_n);
+        const int r = quad * 32 + 16 * la + 8 * hr + g;  // row of the block
+        if (r >= nr) continue;
+        const float rs = nt > 0 ? rests[r] + rests[128 + r] : 0.f;
+        if (S > 1) {
+          float4* dst = reinterpret_cast<float4*>(
+              parts + ((int64_t)blockIdx.x * kBM + r) * D + c0 + 8 * t);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            dst[i] = make_float4(__uint_as_float(y[4 * i]) + rs, __uint_as_float(y[4 * i + 1]) + rs,
+                                 __uint_as_float(y[4 * i + 2]) + rs,
+                                 __uint_as_float(y[4 * i + 3]) + rs);
+          continue;
         }
-        uint4* dst = reinterpret_cast<uint4*>(a.out + row * a.o_rs + h * D + d0);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        const uint32_t v[4] = {vv[hr].x, vv[hr].y, vv[hr].z, vv[hr].w};
+        const bool is_cand = r >= cand;
+        const float own = rd[256 + r];
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y0 = __uint_as_float(y[2 * i]) + rs, y1 = __uint_as_float(y[2 * i + 1]) + rs;
+          if (is_cand) {
+            y0 = fmaf(own, bf_lo(v[i]), y0);
+            y1 = fmaf(own, bf_hi(v[i]), y1);
+          }
+          w[i] = pack_bf16x2(y0 * a.inv_n, y1 * a.inv_n);
+        }
+        *reinterpret_cast<uint4*>(a.out + (row0 + r) * a.o_rs + h * D + c0 + 8 * t) =
+            make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
@@ -655,7 +758,7 @@ cudaError_t launch_tc(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
 
 size_t cache_tc_ws_bytes(const CacheAttnArgs& a, int d) {
   const TcPlan p = tc_plan(a);
-  return p.S == 1 ? 256 : align256((size_t)p.units * p.S * kBM * d * sizeof(float));
+  return p.S == 1 ? 0 : align256((size_t)p.units * p.S * kBM * d * sizeof(float));
 }
 
 cudaError_t launch_cache_tc(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st) {

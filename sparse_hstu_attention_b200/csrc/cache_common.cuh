@@ -73,19 +73,32 @@ struct CacheSeq {
   int s0, n, h, Lh;  // first row, rows, of them history rows, cached tokens
 };
 
-// Reads and checks sequence b; false (and status set) if it is out of range.
-__device__ __forceinline__ bool cache_seq(const CacheAttnArgs& a, int b, CacheSeq* s) {
-  const int o0 = a.offs[b], o1 = a.offs[b + 1];
-  const int nt = a.nts ? a.nts[b] : 0;
-  const int Lh = a.t.lengths[b];
-  s->s0 = o0;
-  s->n = o1 - o0;
-  s->h = s->n - nt;
-  s->Lh = Lh;
-  const bool ok = o0 >= 0 && o1 >= o0 && (int64_t)o1 <= a.T && nt >= 0 && nt <= s->n &&
-                  s->n <= a.max_new && Lh >= s->h && Lh <= a.t.M * a.t.ps;
+// Sequence b's numbers as they stand in memory, and their check: false (and
+// status set) if they are out of range.
+struct CacheSeqRaw {
+  int o0, o1, nt, Lh;
+};
+__device__ __forceinline__ CacheSeqRaw cache_seq_load(const CacheAttnArgs& a, int b) {
+  CacheSeqRaw r;
+  r.o0 = a.offs[b];
+  r.o1 = a.offs[b + 1];
+  r.nt = a.nts ? a.nts[b] : 0;
+  r.Lh = a.t.lengths[b];
+  return r;
+}
+__device__ __forceinline__ bool cache_seq_check(const CacheAttnArgs& a, const CacheSeqRaw& r,
+                                                CacheSeq* s) {
+  s->s0 = r.o0;
+  s->n = r.o1 - r.o0;
+  s->h = s->n - r.nt;
+  s->Lh = r.Lh;
+  const bool ok = r.o0 >= 0 && r.o1 >= r.o0 && (int64_t)r.o1 <= a.T && r.nt >= 0 &&
+                  r.nt <= s->n && s->n <= a.max_new && r.Lh >= s->h && r.Lh <= a.t.M * a.t.ps;
   if (!ok) cache_fail(a.t, HSTU_SLA_ERR_BAD_INPUT);
   return ok;
+}
+__device__ __forceinline__ bool cache_seq(const CacheAttnArgs& a, int b, CacheSeq* s) {
+  return cache_seq_check(a, cache_seq_load(a, b), s);
 }
 
 // Cached keys that row r of a sequence sees: [0, pre) and [lo, hi) (either may

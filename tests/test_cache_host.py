@@ -154,13 +154,15 @@ def test_attend_refusals(lib, field, value, code):
 
 
 def test_attend_workspace_refusals(lib):
-    p = _attend()
-    need = lib.hstu_cache_attend_workspace_bytes(_tables(), p)
+    # two sequences of one row and long histories: the keys are split over blocks
+    p = _attend(total_tokens=4, max_new=1, K1=1 << 20)
+    t = _tables(max_pages=4096)
+    need = lib.hstu_cache_attend_workspace_bytes(t, p)
     assert need >= 256 and need % 256 == 0
     f = lib.hstu_cache_attend
-    assert f(_tables(), p, None, need, None) == _abi.ERR_WORKSPACE
-    assert f(_tables(), p, FAKE + 64, need, None) == _abi.ERR_WORKSPACE
-    assert f(_tables(), p, FAKE, need - 1, None) == _abi.ERR_WORKSPACE
+    assert f(t, p, None, need, None) == _abi.ERR_WORKSPACE
+    assert f(t, p, FAKE + 64, need, None) == _abi.ERR_WORKSPACE
+    assert f(t, p, FAKE, need - 1, None) == _abi.ERR_WORKSPACE
 
 
 def test_binding_structs_match_the_header(tmp_path):
