@@ -28,8 +28,8 @@
 // tiles (V transposed: its bytes lie along the tokens).  Scores are read from
 // TMEM as 16 x 256-bit fragments: a thread has 4 rows and a quarter of the
 // columns, so the per-key pairs are one 16-byte load per two columns and four
-// rows.  The loops over 16-column pieces stay rolled: unrolled, the kernel's code
-// no longer fits the instruction cache, which cost more than the loops do.
+// rows.  The loop over 16-column pieces is unrolled by two only: the code of a
+// kernel that unrolls everything outgrows the instruction cache.
 //
 // Bound: the special-function unit (one tanh a score, 1024 clocks a 128 x 128
 // tile and SM, as long as the tile's products take), then issue slots.
@@ -105,11 +105,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
   return r;
 }
-// Codes in bits 0..3 of the halves, the bf16 subnormals c 2^-133, times 2^127:
-// the bf16 numbers c / 64, exact.
-__device__ __forceinline__ uint32_t code_bf16x2(uint32_t x) {
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x & 0x000f000fu), "r"(0x7f007f00u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
 
@@ -153,10 +151,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int bh = unit / row_tiles, r0 = (unit % row_tiles) * kBM;
   const int b = bh / a.H, h = bh % a.H;
 
+  const int status = cache_status(a.t);
   CacheSeq sq;
   if (!cache_seq(a, b, &sq) || r0 >= sq.n) return;
   // (one status for the whole block, so that its threads part ways together)
-  if (__syncthreads_or(cache_status(a.t) != 0)) return;
+  if (__syncthreads_or(status != 0)) return;
   const int nr = imin(kBM, sq.n - r0);
   const CacheTiles tl = cache_tiles<kBN>(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
   const int bl = (tl.n + S - 1) / S;
@@ -186,12 +185,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int32_t* const bt = a.t.bt + (int64_t)b * a.t.M;
   const uint8_t* const head = a.pages + (int64_t)h * lay.bytes;
 
-  // This head's block of the pages of tiles [32 c, 32 c + 32): null past the
-  // cached tokens.
+  // This head's block of the pages of tiles [32 c, 32 c + 32).  Places past the
+  // cached tokens get page 0's: what is read there is masked.
   auto load_ids = [&](int c) {
     const int n = c * kIdTiles + (tid >> lpt);
     if (tid >= kIdTiles << lpt) return;
-    const uint8_t* p = nullptr;
+    const uint8_t* p = head;
     if (n < nt) {
       const int i = (tl.at(e0 + n) << lpt) + (tid & ((1 << lpt) - 1));
       if (i < pages) {
@@ -208,6 +207,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto entry = [&](int n) -> const uint8_t* const* {
     return blocks + ((n / kIdTiles) & 1) * (kIdTiles * 8) + ((n % kIdTiles) << lpt);
   };
+  // q, and the candidates' k: D / 8 lanes a row, 16 rows a warp.
+  constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;
+  const int ch = lane % LPR, rw = warp * 16 + lane / LPR;
+  const bf16* const qp = a.q + (int64_t)(sq.s0 + r0 + rw) * a.q_rs + h * D + ch * 8;
+  const bf16* const kp = a.k + (int64_t)(sq.s0 + r0 + rw) * a.k_rs + h * D + ch * 8;
+  const int cand = sq.h - r0;  // first candidate row of the block
+  uint4 q[IT], k[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int r = rw + i * RPI;
+    q[i] = k[i] = make_uint4(0, 0, 0, 0);
+    if (r < nr) q[i] = *reinterpret_cast<const uint4*>(qp + (int64_t)i * RPI * a.q_rs);
+    if (r < nr && r >= cand)
+      k[i] = *reinterpret_cast<const uint4*>(kp + (int64_t)i * RPI * a.k_rs);
+  }
   load_ids(0);
   tc_fence_before();
   __syncthreads();
@@ -225,28 +239,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint8_t* const* e = entry(n);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const uint8_t* p = e[k_page + (x ? 64 >> lps : 0)];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) kc[x][w] = 0;
-      if (p) {
-        if constexpr (D == 128) {
-          const uint4 y = *reinterpret_cast<const uint4*>(p + k_off);
-          kc[x][0] = y.x; kc[x][1] = y.y; kc[x][2] = y.z; kc[x][3] = y.w;
-        } else if constexpr (D == 64) {
-          const uint2 y = *reinterpret_cast<const uint2*>(p + k_off);
-          kc[x][0] = y.x; kc[x][1] = y.y;
-        } else {
-          kc[x][0] = *reinterpret_cast<const uint32_t*>(p + k_off);
-        }
+      const uint8_t* p = e[k_page + (x ? 64 >> lps : 0)] + k_off;
+      if constexpr (D == 128) {
+        const uint4 y = *reinterpret_cast<const uint4*>(p);
+        kc[x][0] = y.x; kc[x][1] = y.y; kc[x][2] = y.z; kc[x][3] = y.w;
+      } else if constexpr (D == 64) {
+        const uint2 y = *reinterpret_cast<const uint2*>(p);
+        kc[x][0] = y.x; kc[x][1] = y.y;
+      } else {
+        kc[x][0] = *reinterpret_cast<const uint32_t*>(p);
       }
     }
-    kpar = vpar = 0;
     if (tid < kBN) {
-      const uint8_t* p = e[par_page];
-      if (p) {
-        kpar = *reinterpret_cast<const uint32_t*>(p + par_off);
-        vpar = *reinterpret_cast<const uint32_t*>(p + par_off + 4 * ps);
-      }
+      const uint8_t* p = e[par_page] + par_off;
+      kpar = *reinterpret_cast<const uint32_t*>(p);
+      vpar = *reinterpret_cast<const uint32_t*>(p + 4 * ps);
     }
   };
   // f16 codes into the K tile; the pairs of token tid as floats, column pairs
@@ -285,15 +292,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int v_page = v_tok >> lps, v_off = lay.v + v_i * ps + (v_tok & (ps - 1));
   auto load_v = [&](int n) {
     const uint8_t* const* e = entry(n);
+    if (!v_warp) return;
 #pragma unroll
     for (int x = 0; x < VX; ++x) {
-#pragma unroll
-      for (int w = 0; w < 4; ++w) vc[x][w] = 0;
-      const uint8_t* p = v_warp ? e[v_page + (x ? 64 >> lps : 0)] : nullptr;
-      if (p) {
-        const uint4 y = *reinterpret_cast<const uint4*>(p + v_off);
-        vc[x][0] = y.x; vc[x][1] = y.y; vc[x][2] = y.z; vc[x][3] = y.w;
-      }
+      const uint4 y =
+          *reinterpret_cast<const uint4*>(e[v_page + (x ? 64 >> lps : 0)] + v_off);
+      vc[x][0] = y.x; vc[x][1] = y.y; vc[x][2] = y.z; vc[x][3] = y.w;
     }
   };
   // bf16 codes / 64 into the V tile, rows = dims.  Lanes 0-3 of eight store the even
@@ -302,7 +306,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t v_odd = (lane >> 2) & 1;
   const uint32_t v_row = 2 * v_i + v_odd;
   const uint32_t v_at = sV + v_half * C::BOXV + v_row * 128 + (((2 * (lane >> 3)) ^ (v_row & 7)) << 4);
-  const uint32_t v_sh = 4 * v_odd;
+  // A nibble in bits 0..3 of a half is the bf16 number c 2^-133, in bits 4..7
+  // c 2^-129 (c < 8 subnormal, above normal, one line): times 2^127 or 2^123
+  // both are c / 64, exactly.
+  const uint32_t v_mask[2] = {v_odd ? 0x00f000f0u : 0x000f000fu,
+                              v_odd ? 0x000f000fu : 0x00f000f0u};
+  const uint32_t v_mul[2] = {v_odd ? 0x7d007d00u : 0x7f007f00u,
+                             v_odd ? 0x7f007f00u : 0x7d007d00u};
   auto store_v = [&]() {
     if (!v_warp) return;
 #pragma unroll
@@ -311,12 +321,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int pass = 0; pass < 2; ++pass) {
         // the other dim of the pair: row ^ 1, and so its chunks' places ^ 1
         const uint32_t at = (pass ? v_at ^ 144u : v_at) + x * C::BOXV;
-        const uint32_t sh = pass ? v_sh ^ 4u : v_sh;
         uint32_t r[8];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          r[2 * w] = code_bf16x2(vc[x][w] >> sh);
-          r[2 * w + 1] = code_bf16x2(vc[x][w] >> (sh + 8));
+          r[2 * w] = mul_bf16x2(vc[x][w] & v_mask[pass], v_mul[pass]);
+          r[2 * w + 1] = mul_bf16x2((vc[x][w] >> 8) & v_mask[pass], v_mul[pass]);
         }
         st_shared_v4(at, r[0], r[1], r[2], r[3]);
         st_shared_v4(at ^ 16u, r[4], r[5], r[6], r[7]);
@@ -327,14 +336,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     load_k(0);
     load_v(0);
   }
-  // q into shared memory: D / 8 lanes a row, 16 rows a warp.
+  // q into shared memory (loaded above).
   bool common;
   {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI, UB = IT < 4 ? IT : 4;
-    const int ch = lane % LPR, rw = warp * 16 + lane / LPR;
-    const bf16* qp = a.q + (int64_t)(sq.s0 + r0 + rw) * a.q_rs + h * D + ch * 8;
-    const bf16* kp = a.k + (int64_t)(sq.s0 + r0 + rw) * a.k_rs + h * D + ch * 8;
-    const int cand = sq.h - r0;  // first candidate row of the block
     // 16 bytes of f16 (q times up; the dims of high nibbles over 16) into row r
     auto put = [&](int r, const uint4& y, float up) {
       const uint32_t sw = C::SWK == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
@@ -348,55 +352,42 @@ __global__ void __launch_bounds__(kThreads, 2)
                    pack_f16x2(bf_lo(y.w) * hi, bf_hi(y.w) * hi));
     };
     bool fits = true;
-#pragma unroll 1
-    for (int i0 = 0; i0 < IT; i0 += UB) {
-      uint4 q[UB], k[UB];  // (all loads before the first use)
+    float sum[IT], own[IT];
+    uint32_t most[IT];
 #pragma unroll
-      for (int i = 0; i < UB; ++i) {
-        const int r = rw + (i0 + i) * RPI;
-        q[i] = k[i] = make_uint4(0, 0, 0, 0);
-        if (r < nr) q[i] = *reinterpret_cast<const uint4*>(qp + (int64_t)(i0 + i) * RPI * a.q_rs);
-        if (r < nr && r >= cand)
-          k[i] = *reinterpret_cast<const uint4*>(kp + (int64_t)(i0 + i) * RPI * a.k_rs);
+    for (int i = 0; i < IT; ++i) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+      const uint32_t z[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
+      sum[i] = own[i] = 0.f;
+      most[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[i] += bf_lo(w[j]) + bf_hi(w[j]);
+        own[i] = fmaf(bf_lo(w[j]), bf_lo(z[j]), fmaf(bf_hi(w[j]), bf_hi(z[j]), own[i]));
+        most[i] = umax(most[i], umax(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
       }
-      float sum[UB], own[UB];
-      uint32_t most[UB];
+      put(rw + i * RPI, q[i], 16.f);
+    }
 #pragma unroll
-      for (int i = 0; i < UB; ++i) {
-        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-        const uint32_t z[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
-        sum[i] = own[i] = 0.f;
-        most[i] = 0;
+    for (int o = 1; o < LPR; o <<= 1)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sum[i] += bf_lo(w[j]) + bf_hi(w[j]);
-          own[i] = fmaf(bf_lo(w[j]), bf_lo(z[j]), fmaf(bf_hi(w[j]), bf_hi(z[j]), own[i]));
-          most[i] = umax(most[i], umax(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
-        }
-        put(rw + (i0 + i) * RPI, q[i], 16.f);
+      for (int i = 0; i < IT; ++i) {
+        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        own[i] += __shfl_xor_sync(0xffffffffu, own[i], o);
+        most[i] = umax(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
       }
+    if (ch == 0) {
 #pragma unroll
-      for (int o = 1; o < LPR; o <<= 1)
-#pragma unroll
-        for (int i = 0; i < UB; ++i) {
-          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-          own[i] += __shfl_xor_sync(0xffffffffu, own[i], o);
-          most[i] = umax(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
-        }
-#pragma unroll
-      for (int i = 0; i < UB; ++i) {
-        const int r = rw + (i0 + i) * RPI;
+      for (int i = 0; i < IT; ++i) {
+        const int r = rw + i * RPI;
         // most in [2^-6, 2^11), or a row of zeros: 2^4 will do; else the row's
         // largest goes to [2^14, 2^15) (values below 2^-112: times 2^126)
         fits = fits && (most[i] == 0 || (most[i] >= 121u << 7 && most[i] < 138u << 7));
-        if (ch == 0) {
-          const int e = imax((int)(most[i] >> 7) - 127, -112);
-          rd[r] = __int_as_float(imin(117 + e, 254) << 23);  // 2^(e - 10)
-          rd[128 + r] =
-              most[i] >= 0x7f80u ? __int_as_float(0x7fc00000) : sum[i] * (0.5f * a.alpha);
-          const float y = own[i] * a.alpha;
-          rd[256 + r] = r >= cand ? __fdividef(y, 1.f + __expf(-y)) : 0.f;
-        }
+        const int e = imax((int)(most[i] >> 7) - 127, -112);
+        rd[r] = __int_as_float(imin(117 + e, 254) << 23);  // 2^(e - 10)
+        rd[128 + r] = most[i] >= 0x7f80u ? __int_as_float(0x7fc00000) : sum[i] * (0.5f * a.alpha);
+        const float y = own[i] * a.alpha;
+        rd[256 + r] = r >= cand ? __fdividef(y, 1.f + __expf(-y)) : 0.f;
       }
     }
     common = __syncthreads_and(fits);
@@ -404,9 +395,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
       for (int i = 0; i < IT; ++i) {
         const int r = rw + i * RPI;
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (r < nr) q = *reinterpret_cast<const uint4*>(qp + (int64_t)i * RPI * a.q_rs);
-        put(r, q, 16.f / rd[r]);
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (r < nr) y = *reinterpret_cast<const uint4*>(qp + (int64_t)i * RPI * a.q_rs);
+        put(r, y, 16.f / rd[r]);
       }
     }
   }
@@ -483,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // FAST: every pair visible, one factor for all rows (in the steps s)
       auto pointwise = [&](auto fast) {
         constexpr bool FAST = decltype(fast)::value;
-#pragma unroll 1
+#pragma unroll 2
         for (int cg = 0; cg < 4; ++cg) {  // 16 columns each
           const uint32_t at = lanes + kColS + chalf * 64 + cg * 16;
           uint32_t s0[8], s1[8];
@@ -576,20 +567,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   {
     constexpr int NA = D >= 64 ? 2 : 1, NC = D == 128 ? 2 : 1;
     const int64_t row0 = sq.s0 + r0;
-    const int cand = sq.h - r0;  // first candidate row
-#pragma unroll 1
+    uint4 vv[NA * NC][2];  // the candidates' v: all loads before the first use
+#pragma unroll
+    for (int i = 0; i < NA * NC * 2; ++i) {
+      const int la = D >= 64 ? (i >> 1) / NC : chalf;
+      const int c0 = D >= 64 ? (chalf * NC + (i >> 1) % NC) * 32 : 0;
+      const int r = quad * 32 + 16 * la + 8 * (i & 1) + g;
+      vv[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+      if (S == 1 && r >= cand && r < nr)
+        vv[i >> 1][i & 1] =
+            *reinterpret_cast<const uint4*>(a.v + (row0 + r) * a.v_rs + h * D + c0 + 8 * t);
+    }
+#pragma unroll
     for (int ac = 0; ac < NA * NC; ++ac) {
       const int la = D >= 64 ? ac / NC : chalf;                 // 16 lanes of the quarter
       const int c0 = D >= 64 ? (chalf * NC + ac % NC) * 32 : 0;  // 32 dims
-      uint4 vv[2];  // the candidates' v
-#pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const int r = quad * 32 + 16 * la + 8 * hr + g;
-        vv[hr] = make_uint4(0, 0, 0, 0);
-        if (S == 1 && r >= cand && r < nr)
-          vv[hr] = *reinterpret_cast<const uint4*>(a.v + (row0 + r) * a.v_rs + h * D +
-                                                   c0 + 8 * t);
-      }
       uint32_t oa[8], ob[8];
       if (nt > 0) {
         const uint32_t at = lanes + ((uint32_t)(16 * la) << 16) + kColO + c0;
@@ -637,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                  __uint_as_float(y[4 * i + 3]) + rs);
           continue;
         }
-        const uint32_t v[4] = {vv[hr].x, vv[hr].y, vv[hr].z, vv[hr].w};
+        const uint32_t v[4] = {vv[ac][hr].x, vv[ac][hr].y, vv[ac][hr].z, vv[ac][hr].w};
         const bool is_cand = r >= cand;
         const float own = rd[256 + r];
         uint32_t w[4];
