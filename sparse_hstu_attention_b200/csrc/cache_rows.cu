@@ -2,8 +2,12 @@
 //
 // A block takes TT consecutive rows of one head; D / 8 lanes hold a row, 8
 // dims (one word of K codes) each.  Append: the row's minimum and maximum by
-// shuffles, then code = round((x - m) * (1 / s)); read: bf16(m + s code), one
-// fused multiply-add, exact before the rounding to bf16 up to fp32.
+// shuffles, then code = round((x - m) * (1 / s)), the rounding to whole numbers
+// by adding 1.5 2^23 and the packing of 8 codes by multiply-adds with powers of
+// 16 (mod 2^32; what the added constant leaves is taken off at the end).  Even
+// lanes divide for K and odd ones for V.  Read: bf16(m + s code) by one bf16
+// multiply-add, which rounds once; since s code has at most 12 bits, that is
+// also what fp32 rounded to bf16 gives.
 //
 // V codes lie dim pair by dim pair, so one row's bytes are page_size apart.
 // Rows of one sequence come in runs of consecutive slots: a run's part in one
@@ -11,7 +15,8 @@
 // by column, and moves as 16-byte pieces.  A tile with too many groups (single
 // events of many users) moves single bytes.
 //
-// Bound: bytes (append reads 4 d and writes d + 8 per token and head).
+// Bound: bytes (append reads 4 d and writes d + 8 per token and head), with
+// issue slots close behind.
 #include "cache_common.cuh"
 
 namespace hstu {
@@ -24,7 +29,8 @@ template <int TT>
 struct Groups {
   static constexpr int kMost = TT / 16 + 8;  // groups a tile may hold in shared memory
   static constexpr int kPitch = kMost * 16 + 4;
-  int64_t slot[TT];    // -1: no row
+  int64_t slot[TT];         // -1: no row
+  uint8_t* block[TT];       // this head's block of the slot's page
   int16_t group[TT];
   uint32_t mask[kMost];     // places of the group that have a row
   int64_t base[kMost];      // its first slot, a multiple of 16
@@ -33,7 +39,8 @@ struct Groups {
 
 // Slots of the tile's rows, checked; groups numbered.  Returns their count.
 template <int TT>
-__device__ __forceinline__ int find_groups(const CacheRowArgs& a, int64_t t0, Groups<TT>* g) {
+__device__ __forceinline__ int find_groups(const CacheRowArgs& a, int64_t t0, int head_off,
+                                           Groups<TT>* g) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n_slots = (int64_t)a.t.P << a.t.lps;
   if (tid < TT) {
@@ -42,7 +49,9 @@ __device__ __forceinline__ int find_groups(const CacheRowArgs& a, int64_t t0, Gr
       cache_fail(a.t, HSTU_SLA_ERR_BAD_INPUT);
       s = -1;
     }
-    g->slot[tid] = s < 0 ? -1 : s;
+    s = s < 0 ? -1 : s;
+    g->slot[tid] = s;
+    g->block[tid] = a.pages + (s < 0 ? 0 : s >> a.t.lps) * a.page_stride + head_off;
   }
   if (tid < Groups<TT>::kMost) g->mask[tid] = 0;
   __syncthreads();
@@ -75,57 +84,67 @@ __device__ __forceinline__ int find_groups(const CacheRowArgs& a, int64_t t0, Gr
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// Codes of the lane's 8 dims and the row's (step, minimum) pair: nibble n of
-// *word is dim n.  LPR lanes hold one row.
-template <int LPR>
-__device__ __forceinline__ void quantise(const uint4& x, uint32_t* word, uint32_t* pair) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float f[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = bf_lo(w[e]);
-    f[2 * e + 1] = bf_hi(w[e]);
-  }
-  // minimum and maximum in bf16 pairs (exact); a NaN stays one
-  const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(w);
-  __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(b[0], b[1]), __hmin2_nan(b[2], b[3]));
-  __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(b[0], b[1]), __hmax2_nan(b[2], b[3]));
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) {
-    lo2 = __hmin2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, o));
-    hi2 = __hmax2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, o));
-  }
-  float m = __bfloat162float(__hmin_nan(lo2.x, lo2.y));
-  const float hi = __bfloat162float(__hmax_nan(hi2.x, hi2.y));
-  float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, m), 15.f)));
-  const bool fine = s <= 3.4e38f;  // not for a NaN or an infinity
-  if (s < 1.17549435e-38f) s = 0.f;
-  const float inv = s > 0.f && fine ? __frcp_rn(s) : 0.f;
-  uint32_t c = 0;
-  if (fine) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int v = __float2int_rn(__fmul_rn(__fsub_rn(f[e], m), inv));
-      c |= (uint32_t)imin(v, 15) << (4 * e);
-    }
-  } else {
-    s = m = __int_as_float(0x7fc00000);
-  }
-  *word = c;
-  const __nv_bfloat162 sm = __floats2bfloat162_rn(s, m);
-  *pair = *reinterpret_cast<const uint32_t*>(&sm);
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 x) {
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ __nv_bfloat162 pair(uint32_t x) {
+  return *reinterpret_cast<const __nv_bfloat162*>(&x);
 }
 
-// Nibbles (dim n at n) to the order of a K word: dims 0 2 4 6 1 3 5 7.
-__device__ __forceinline__ uint32_t k_word(uint32_t c) {
-  uint32_t r = 0;
+// (minimum, -maximum) of a row as bf16 (exact); a NaN stays one.
+template <int LPR>
+__device__ __forceinline__ uint32_t extremes(const uint32_t (&w)[4]) {
+  const __nv_bfloat162 lo = __hmin2_nan(__hmin2_nan(pair(w[0]), pair(w[1])),
+                                        __hmin2_nan(pair(w[2]), pair(w[3])));
+  const __nv_bfloat162 hi = __hmax2_nan(__hmax2_nan(pair(w[0]), pair(w[1])),
+                                        __hmax2_nan(pair(w[2]), pair(w[3])));
+  const uint32_t x = __byte_perm(bits(lo), bits(hi), 0x5410) ^ 0x80000000u;
+  const uint32_t y = __byte_perm(bits(lo), bits(hi), 0x7632) ^ 0x80000000u;
+  uint32_t r = bits(__hmin2_nan(pair(x), pair(y)));
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    r |= ((c >> (8 * n)) & 15u) << (4 * n);
-    r |= ((c >> (8 * n + 4)) & 15u) << (16 + 4 * n);
-  }
+  for (int o = LPR / 2; o > 0; o >>= 1)
+    r = bits(__hmin2_nan(pair(r), pair(__shfl_xor_sync(0xffffffffu, r, o))));
   return r;
+}
+
+// Codes of 8 dims, dim i at nibble i (K: at the nibble of a K word).
+template <bool K>
+__device__ __forceinline__ uint32_t codes(const uint32_t (&w)[4], float m, float inv) {
+  constexpr uint32_t kMagic = 0x4b400000u;  // 1.5 2^23
+  uint32_t c = 0u - kMagic * 0x11111111u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x = __fsub_rn(bf_lo(w[e]), m), y = __fsub_rn(bf_hi(w[e]), m);
+    x = __fadd_rn(__fmul_rn(x, inv), __uint_as_float(kMagic));
+    y = __fadd_rn(__fmul_rn(y, inv), __uint_as_float(kMagic));
+    c += __float_as_uint(x) * (1u << (K ? 4 * e : 8 * e));
+    c += __float_as_uint(y) * (1u << (K ? 4 * e + 16 : 8 * e + 4));
+  }
+  return c;
+}
+
+// A token's K and V rows: the lane's codes and the rows' (step, minimum) pairs.
+template <int LPR>
+__device__ __forceinline__ void quantise(const uint4& xk, const uint4& xv, uint32_t* ck,
+                                         uint32_t* cv, uint32_t* pk, uint32_t* pv) {
+  const uint32_t k[4] = {xk.x, xk.y, xk.z, xk.w}, v[4] = {xv.x, xv.y, xv.z, xv.w};
+  const uint32_t ek = extremes<LPR>(k), ev = extremes<LPR>(v);
+  const bool odd = threadIdx.x & 1;
+  const uint32_t e = odd ? ev : ek;
+  float s = __bfloat162float(
+      __float2bfloat16_rn(__fdiv_rn(__fsub_rn(-bf_hi(e), bf_lo(e)), 15.f)));
+  if (s < 1.17549435e-38f) s = 0.f;
+  // not for a NaN or an infinity: such a row is NaN, its codes 0
+  const bool fine = s <= 3.4e38f;
+  const float inv = !fine ? __int_as_float(0x7fc00000) : s > 0.f ? __frcp_rn(s) : 0.f;
+  const uint32_t p = fine ? (__float_as_uint(s) >> 16) | (e << 16) : 0x7fc07fc0u;
+  const float inv2 = __shfl_xor_sync(0xffffffffu, inv, 1);
+  const uint32_t p2 = __shfl_xor_sync(0xffffffffu, p, 1);
+  const float ik = odd ? inv2 : inv, iv = odd ? inv : inv2;
+  *pk = odd ? p2 : p;
+  *pv = odd ? p : p2;
+  *ck = isnan(ik) ? 0u : codes<true>(k, bf_lo(ek), ik);
+  *cv = isnan(iv) ? 0u : codes<false>(v, bf_lo(ev), iv);
 }
 
 template <int D, int TT>
@@ -138,7 +157,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheRowArgs a) 
   const int64_t t0 = (int64_t)blockIdx.x * TT;
   const int h = blockIdx.y, ps = a.t.ps;
   const PageLayout<D> lay(ps);
-  const int n_groups = find_groups<TT>(a, t0, &g);
+  const int n_groups = find_groups<TT>(a, t0, h * lay.bytes, &g);
   const bool grouped = n_groups <= G::kMost;
   const int w = threadIdx.x % LPR;
 #pragma unroll 2
@@ -150,12 +169,11 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheRowArgs a) 
       xv = *reinterpret_cast<const uint4*>(a.v + (t0 + r0) * a.v_rs + h * D + w * 8);
     }
     uint32_t ck, pk, cv, pv;
-    quantise<LPR>(xk, &ck, &pk);
-    quantise<LPR>(xv, &cv, &pv);
+    quantise<LPR>(xk, xv, &ck, &cv, &pk, &pv);
     if (s < 0) continue;
-    uint8_t* blk = a.pages + (s >> a.t.lps) * a.page_stride + (int64_t)h * lay.bytes;
+    uint8_t* blk = g.block[r0];
     const int r = (int)s & (ps - 1);
-    *reinterpret_cast<uint32_t*>(blk + r * (D / 2) + w * 4) = k_word(ck);
+    *reinterpret_cast<uint32_t*>(blk + r * (D / 2) + w * 4) = ck;
     if (w == 0) {
       *reinterpret_cast<uint32_t*>(blk + lay.kp + 4 * r) = pk;
       *reinterpret_cast<uint32_t*>(blk + lay.vp + 4 * r) = pv;
@@ -196,18 +214,12 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(CacheRowArgs a) 
   }
 }
 
-// 8 values m + s code (nibble n of c is dim n), rounded to bf16.
-__device__ __forceinline__ uint4 dequantise(uint32_t c, uint32_t pair) {
-  const float s = bf_lo(pair), m = bf_hi(pair);
-  uint32_t o[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 v =
-        __floats2bfloat162_rn(fmaf(s, (float)((c >> (8 * e)) & 15u), m),
-                              fmaf(s, (float)((c >> (8 * e + 4)) & 15u), m));
-    o[e] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+// Two values m + s code, the codes in bits 0..3 of the halves: 128 + c is a bf16
+// number with c in its last bits.
+__device__ __forceinline__ uint32_t dequantise(uint32_t c, __nv_bfloat162 s, __nv_bfloat162 m) {
+  const __nv_bfloat162 x =
+      __hadd2_rn(pair((c & 0x000f000fu) | 0x43004300u), pair(0xc300c300u));
+  return bits(__hfma2(x, s, m));
 }
 
 template <int D, int TT>
@@ -220,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheRowArgs a) {
   const int64_t t0 = (int64_t)blockIdx.x * TT;
   const int h = blockIdx.y, ps = a.t.ps;
   const PageLayout<D> lay(ps);
-  const int n_groups = find_groups<TT>(a, t0, &g);
+  const int n_groups = find_groups<TT>(a, t0, h * lay.bytes, &g);
   const bool grouped = n_groups <= G::kMost;
   if (grouped) {
     for (int e = threadIdx.x; e < n_groups * (D / 2); e += kThreads) {
@@ -244,22 +256,24 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheRowArgs a) {
     const int64_t s = g.slot[r0];
     uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
     if (s >= 0) {
-      const uint8_t* blk = a.pages + (s >> a.t.lps) * a.page_stride + (int64_t)h * lay.bytes;
+      const uint8_t* blk = g.block[r0];
       const int r = (int)s & (ps - 1);
       const uint32_t kw = *reinterpret_cast<const uint32_t*>(blk + r * (D / 2) + w * 4);
-      uint32_t ck = 0, cv = 0;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        ck |= ((kw >> (4 * n)) & 15u) << (8 * n);
-        ck |= ((kw >> (16 + 4 * n)) & 15u) << (8 * n + 4);
-      }
+      const uint32_t kp = *reinterpret_cast<const uint32_t*>(blk + lay.kp + 4 * r);
+      const uint32_t vp = *reinterpret_cast<const uint32_t*>(blk + lay.vp + 4 * r);
       const uint8_t* col = grouped ? sv + 4 * w * G::kPitch + g.group[r0] * 16 + v_place(r & 15)
                                    : blk + lay.v + 4 * w * ps + v_place(r);
       const int step = grouped ? G::kPitch : ps;
+      uint32_t b[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) cv |= (uint32_t)col[e * step] << (8 * e);
-      xk = dequantise(ck, *reinterpret_cast<const uint32_t*>(blk + lay.kp + 4 * r));
-      xv = dequantise(cv, *reinterpret_cast<const uint32_t*>(blk + lay.vp + 4 * r));
+      for (int e = 0; e < 4; ++e) b[e] = col[e * step];
+      __nv_bfloat162 s2 = pair(__byte_perm(kp, 0, 0x1010)), m2 = pair(__byte_perm(kp, 0, 0x3232));
+      xk = make_uint4(dequantise(kw, s2, m2), dequantise(kw >> 4, s2, m2),
+                      dequantise(kw >> 8, s2, m2), dequantise(kw >> 12, s2, m2));
+      s2 = pair(__byte_perm(vp, 0, 0x1010));
+      m2 = pair(__byte_perm(vp, 0, 0x3232));
+      xv = make_uint4(dequantise(b[0] | b[0] << 12, s2, m2), dequantise(b[1] | b[1] << 12, s2, m2),
+                      dequantise(b[2] | b[2] << 12, s2, m2), dequantise(b[3] | b[3] << 12, s2, m2));
     }
     *reinterpret_cast<uint4*>(a.k + (t0 + r0) * a.k_rs + h * D + w * 8) = xk;
     *reinterpret_cast<uint4*>(a.v + (t0 + r0) * a.v_rs + h * D + w * 8) = xv;
