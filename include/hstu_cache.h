@@ -63,7 +63,7 @@ extern "C" {
  *                [i page_size, (i + 1) page_size) at entry i */
 typedef struct {
   int32_t B;          /* >= 1 */
-  int32_t max_pages;  /* per sequence, 1 .. 2^20 */
+  int32_t max_pages;  /* per sequence, 1 .. 2^19 */
   int32_t num_pages;  /* >= 1 */
   int32_t page_size;  /* 16, 32 or 64 */
   int32_t* status;
@@ -74,8 +74,9 @@ typedef struct {
 } hstu_cache_tables;
 
 /* Workspace of hstu_cache_plan: 256-byte aligned, contents need not be
- * initialised.  0 on invalid arguments. */
-size_t hstu_cache_plan_workspace_bytes(int32_t B);
+ * initialised.  0: the call needs none (NULL will do), or the arguments are
+ * invalid. */
+size_t hstu_cache_plan_workspace_bytes(int32_t B, int64_t total_tokens);
 
 /* One step's plan.  Sequence b brings the rows [seq_offsets[b],
  * seq_offsets[b + 1]) of the step's batch, the last num_targets[b] of them

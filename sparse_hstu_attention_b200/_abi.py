@@ -211,7 +211,7 @@ def load():
     lib.hstu_quant_weight_e4m3.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp]
     lib.hstu_quant_weight_e4m3.restype = ctypes.c_int
     tab = ctypes.POINTER(CacheTablesC)
-    lib.hstu_cache_plan_workspace_bytes.argtypes = [i32]
+    lib.hstu_cache_plan_workspace_bytes.argtypes = [i32, i64]
     lib.hstu_cache_plan_workspace_bytes.restype = sz
     lib.hstu_cache_plan.argtypes = [tab, vp, vp, vp, i64, vp, vp, sz, vp]
     lib.hstu_cache_plan.restype = ctypes.c_int

@@ -184,17 +184,22 @@ def plan(tables: CacheTables, seq_offsets: torch.Tensor, num_targets: Optional[t
     rel = _i32(release, tables.B, "release", dev)
     slots = _slots_out(slots, total_tokens, dev)
     lib = _abi.load()
-    ws = _workspace(workspace, lib.hstu_cache_plan_workspace_bytes(tables.B), dev, stream)
+    ws = _workspace(workspace, lib.hstu_cache_plan_workspace_bytes(tables.B, total_tokens), dev,
+                    stream)
     _launch(dev, stream, "hstu_cache_plan", lib.hstu_cache_plan, tables._c, o, nt, rel,
-            total_tokens, slots.data_ptr(), ws.data_ptr(), ws.numel())
+            total_tokens, slots.data_ptr(), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())
     return slots
 
 
-def _workspace(workspace: Optional[torch.Tensor], need: int, dev, stream) -> torch.Tensor:
+def _workspace(workspace: Optional[torch.Tensor], need: int, dev, stream):
     """The given workspace, checked, or a new one (kept from reuse until
-    `stream`, if another than the current one, is done with it)."""
+    `stream`, if another than the current one, is done with it); None if the call
+    needs none."""
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        if need == 0:
+            return None
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         if stream is not None:
             workspace.record_stream(stream)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or \
@@ -257,9 +262,9 @@ def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
     _slots(slots, dev)
     T = slots.numel()
     if k is None:
-        k = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+        k = torch.empty(T, H, d, dtype=torch.bfloat16, device=dev)
     if v is None:
-        v = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+        v = torch.empty_like(k, memory_format=torch.contiguous_format)
     r = _row_call(k, v, slots, pages, tables, H, d, stride)
     _launch(dev, stream, "hstu_cache_read", _abi.load().hstu_cache_read, tables._c, r)
     return k, v
@@ -288,7 +293,7 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
         k_rs, v_rs = _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev)
         k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
     if out is None:
-        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     p = _abi.CacheAttendParams(
         H, d, T, T if max_new is None else int(max_new),
         _i32(seq_offsets, tables.B + 1, "seq_offsets", dev),
@@ -296,10 +301,7 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
         float(alpha), float(N), q.data_ptr(), k_ptr, v_ptr, q_rs, k_rs, v_rs, pages.data_ptr(),
         stride, out.data_ptr(), _rows(out, "out", T, H, d, dev))
     lib = _abi.load()
-    need = lib.hstu_cache_attend_workspace_bytes(tables._c, p)
-    ws = None
-    if need or workspace is not None:
-        ws = _workspace(workspace, need, dev, stream)
+    ws = _workspace(workspace, lib.hstu_cache_attend_workspace_bytes(tables._c, p), dev, stream)
     _launch(dev, stream, "hstu_cache_attend", lib.hstu_cache_attend, tables._c, p,
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out

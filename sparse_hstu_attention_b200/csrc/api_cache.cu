@@ -6,7 +6,7 @@
 #include "cache_common.cuh"
 
 namespace hstu {
-size_t cache_plan_ws_bytes(int B);
+size_t cache_plan_ws_bytes(int B, int64_t T);
 }
 
 using namespace hstu;
@@ -20,7 +20,7 @@ int make_tab(const hstu_cache_tables* t, CacheTab* c) {
   if (t->page_size != 16 && t->page_size != 32 && t->page_size != 64)
     return HSTU_SLA_ERR_UNSUPPORTED;
   if (t->B < 1 || t->num_pages < 1 || t->max_pages < 1) return HSTU_SLA_ERR_INVALID_ARG;
-  if (t->max_pages > (1 << 20)) return HSTU_SLA_ERR_UNSUPPORTED;
+  if (t->max_pages > (1 << 19)) return HSTU_SLA_ERR_UNSUPPORTED;
   const void* ptrs[] = {t->status, t->free_count, t->lengths, t->free_pages, t->block_table};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned(p, 4)) return HSTU_SLA_ERR_INVALID_ARG;
@@ -126,7 +126,9 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? HSTU_SLA_OK : HSTU_SLA_
 
 extern "C" {
 
-size_t hstu_cache_plan_workspace_bytes(int32_t B) { return B < 1 ? 0 : cache_plan_ws_bytes(B); }
+size_t hstu_cache_plan_workspace_bytes(int32_t B, int64_t total_tokens) {
+  return B < 1 || total_tokens < 0 ? 0 : cache_plan_ws_bytes(B, total_tokens);
+}
 
 int hstu_cache_plan(const hstu_cache_tables* t, const int32_t* seq_offsets,
                     const int32_t* num_targets, const int32_t* release, int64_t total_tokens,
@@ -138,8 +140,8 @@ int hstu_cache_plan(const hstu_cache_tables* t, const int32_t* seq_offsets,
   if (seq_offsets == nullptr || total_tokens < 0) return HSTU_SLA_ERR_INVALID_ARG;
   if (total_tokens > INT32_MAX) return HSTU_SLA_ERR_UNSUPPORTED;
   if (total_tokens > 0 && (slots == nullptr || !aligned(slots, 8))) return HSTU_SLA_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned(workspace, 256) ||
-      workspace_bytes < cache_plan_ws_bytes(c.B))
+  const size_t need = cache_plan_ws_bytes(c.B, total_tokens);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need))
     return HSTU_SLA_ERR_WORKSPACE;
   return status_of(launch_cache_plan(c, seq_offsets, num_targets, release, total_tokens, slots,
                                      workspace, reinterpret_cast<cudaStream_t>(stream)));

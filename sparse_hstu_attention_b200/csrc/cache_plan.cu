@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 
-// Per-sequence sums of the plan, in the caller's workspace.
+// Per-sequence sums of the plan, in shared memory or the caller's workspace.
 struct PlanWs {
   int32_t ok;       // 0: the plan failed, nothing below holds
   int32_t top;      // free_count + pages given back, before any is taken
@@ -79,8 +79,9 @@ __device__ __forceinline__ int last_at_most(const int32_t* x, int n, int v) {
   return lo;
 }
 
-// The block's part: checks, sums, new lengths and stack height.  All or
-// nothing: the tables change only if every sequence's step can be done.
+// The block's part: checks, sums and the new stack height.  All or nothing: the tables change only if every sequence's step can be done.
+// PER sequences a thread at a time, so that most batches take one scan.
+template <int PER>
 __device__ bool plan_sums(const PlanArgs& a) {
   __shared__ int sm[2][32];
   __shared__ int s_code;
@@ -89,38 +90,51 @@ __device__ bool plan_sums(const PlanArgs& a) {
   if (threadIdx.x == 0) s_code = fc < 0 || fc > t.P ? HSTU_SLA_ERR_BAD_INPUT : 0;
   __syncthreads();
   int64_t base_need = 0, base_given = 0;
-  for (int c = 0; c < t.B; c += kThreads) {
-    const int b = c + threadIdx.x;
-    int need = 0, given = 0, old = 0;
-    if (b < t.B) {
+  for (int c = 0; c < t.B; c += PER * kThreads) {
+    const int b0 = c + PER * (int)threadIdx.x;
+    int need[PER], given[PER], old[PER], n_sum = 0, g_sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = b0 + i;
+      need[i] = given[i] = old[i] = 0;
+      if (b >= t.B) continue;
       const int o0 = a.offs[b], o1 = a.offs[b + 1], len = t.lengths[b];
       const int nt = a.nts ? a.nts[b] : 0;
       const bool rel = a.release && a.release[b] != 0;
       const int most = t.M * t.ps;
       const bool bad = (b == 0 && o0 != 0) || o0 < 0 || o1 < o0 || (int64_t)o1 > a.T || nt < 0 ||
                        nt > o1 - o0 || len < 0 || len > most;
-      old = rel ? 0 : len;
-      const int fresh = bad ? 0 : o1 - o0 - nt;
-      if (bad || fresh > most - old) {
+      const int fresh = bad ? 0 : o1 - o0 - nt, keep = rel || bad ? 0 : len;
+      if (bad || fresh > most - keep) {
         s_code = HSTU_SLA_ERR_BAD_INPUT;
-        old = 0;
-      } else {
-        need = ((old + fresh + t.ps - 1) >> t.lps) - ((old + t.ps - 1) >> t.lps);
-        given = rel ? (len + t.ps - 1) >> t.lps : 0;
+        continue;
       }
+      old[i] = keep;
+      need[i] = ((keep + fresh + t.ps - 1) >> t.lps) - ((keep + t.ps - 1) >> t.lps);
+      given[i] = rel ? (len + t.ps - 1) >> t.lps : 0;
+    }
+    // (at most 2^19 pages a sequence, max_pages: 4096 of them fit 32 bits; over
+    // the rounds the sums are held at 2^31 - 1, above any num_pages, where the
+    // step fails anyway)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      n_sum += need[i];
+      g_sum += given[i];
     }
     int xn, xg, tn, tg;
-    block_scan2(need, given, &xn, &xg, &tn, &tg, sm);
-    // a chunk's sums stay below 1024 * 2^20 (max_pages); over the chunks they
-    // are held at 2^31 - 1, above any num_pages, where the step fails anyway
+    block_scan2(n_sum, g_sum, &xn, &xg, &tn, &tg, sm);
     const int64_t most = 0x7fffffff;
-    if (b < t.B) {
-      a.old[b] = old;
-      a.need_sum[b] = (int32_t)min(base_need + xn, most);
-      a.given_sum[b] = (int32_t)min(base_given + xg, most);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (b0 + i >= t.B) continue;
+      a.old[b0 + i] = old[i];
+      a.need_sum[b0 + i] = (int32_t)min(base_need + (uint32_t)xn, most);
+      a.given_sum[b0 + i] = (int32_t)min(base_given + (uint32_t)xg, most);
+      xn += need[i];
+      xg += given[i];
     }
-    base_need = min(base_need + tn, most);
-    base_given = min(base_given + tg, most);
+    base_need = min(base_need + (uint32_t)tn, most);
+    base_given = min(base_given + (uint32_t)tg, most);
   }
   if (threadIdx.x == 0) {
     a.need_sum[t.B] = (int32_t)base_need;
@@ -132,10 +146,6 @@ __device__ bool plan_sums(const PlanArgs& a) {
   }
   __syncthreads();
   const bool ok = s_code == 0;
-  if (ok) {
-    for (int b = threadIdx.x; b < t.B; b += kThreads)
-      t.lengths[b] = a.old[b] + a.offs[b + 1] - a.offs[b] - (a.nts ? a.nts[b] : 0);
-  }
   if (threadIdx.x == 0) {
     a.ws->ok = ok;
     a.ws->top = fc + (int)base_given;
@@ -148,67 +158,153 @@ __device__ bool plan_sums(const PlanArgs& a) {
   return ok;
 }
 
-// Released page e (of ws->given) onto the stack.
-__device__ __forceinline__ void plan_push(const PlanArgs& a, int old_top, int e) {
-  const int b = last_at_most(a.given_sum, a.t.B - 1, e);
-  a.t.free_pages[old_top + e] = a.t.bt[(int64_t)b * a.t.M + e - a.given_sum[b]];
+// Released sequence b's pages onto the stack, by a warp.
+__device__ __forceinline__ void plan_push(const PlanArgs& a, int old_top, int b, int lane) {
+  const int from = a.given_sum[b], n = a.given_sum[b + 1] - from;
+  const int32_t* src = a.t.bt + (int64_t)b * a.t.M;
+#pragma unroll 4
+  for (int i = lane; i < n; i += 32) a.t.free_pages[old_top + from + i] = src[i];
 }
 
-// Row `row`: its slot, and the block-table entry if it is the first token of
-// a page.  Entries below `have` are only read and the others only written, so
-// rows need no order among them.
-__device__ __forceinline__ void plan_row(const PlanArgs& a, int top, int64_t row) {
-  int64_t slot = -1;
+__device__ __forceinline__ void plan_length(const PlanArgs& a, int b) {
+  a.t.lengths[b] = a.old[b] + a.offs[b + 1] - a.offs[b] - (a.nts ? a.nts[b] : 0);
+}
+
+// N rows, row[i] of sequence b[i] (negative: -1 it is): their slots, and the
+// block-table entries of those that are the first token of a page.  Entries below
+// `have` are only read and the others only written, so rows need no order among
+// them.  All rows' loads of one kind go out together.
+template <int N>
+__device__ __forceinline__ void plan_rows(const PlanArgs& a, int top, const int64_t (&row)[N],
+                                          const int (&b)[N], int64_t (&slot)[N]) {
   const CacheTab& t = a.t;
-  const int b = row < a.offs[t.B] ? last_at_most(a.offs, t.B - 1, (int)row) : -1;
-  if (b >= 0) {
-    const int r = (int)row - a.offs[b];
-    const int fresh = a.offs[b + 1] - a.offs[b] - (a.nts ? a.nts[b] : 0);
-    if (r < fresh) {
-      const int old = a.old[b], pos = old + r;
-      const int j = pos >> t.lps, have = (old + t.ps - 1) >> t.lps;
-      int page;
-      if (j < have) {
-        page = t.bt[(int64_t)b * t.M + j];
-      } else {
-        page = t.free_pages[top - 1 - (a.need_sum[b] + j - have)];
-        if ((pos & (t.ps - 1)) == 0) t.bt[(int64_t)b * t.M + j] = page;
-      }
-      slot = (int64_t)page * t.ps + (pos & (t.ps - 1));
-    }
+  int o0[N], fresh[N], old[N], taken[N], page[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int x = imax(b[i], 0);
+    o0[i] = a.offs[x];
+    fresh[i] = a.offs[x + 1];
+    old[i] = a.old[x];
+    taken[i] = a.need_sum[x];
   }
-  a.slots[row] = slot;
+  if (a.nts) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) fresh[i] -= a.nts[imax(b[i], 0)];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int pos = old[i] + (int)row[i] - o0[i];
+    const int j = pos >> t.lps, have = (old[i] + t.ps - 1) >> t.lps;
+    const bool mine = b[i] >= 0 && row[i] < fresh[i];
+    const int32_t* src = j < have ? t.bt + (int64_t)b[i] * t.M + j
+                                  : t.free_pages + (top - 1 - (taken[i] + j - have));
+    page[i] = mine ? *src : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int pos = old[i] + (int)row[i] - o0[i];
+    const int j = pos >> t.lps, have = (old[i] + t.ps - 1) >> t.lps, at = pos & (t.ps - 1);
+    const bool mine = b[i] >= 0 && row[i] < fresh[i];
+    if (mine && j >= have && at == 0) t.bt[(int64_t)b[i] * t.M + j] = page[i];
+    slot[i] = mine ? (int64_t)page[i] * t.ps + at : -1;
+  }
 }
 
+// Steps of up to kOneBlockRows rows and kOneBlockSeqs sequences: one block, the
+// sums in shared memory.
+constexpr int64_t kOneBlockRows = 8192;
+constexpr int kOneBlockSeqs = 2048;
+template <int PER>
 __global__ void __launch_bounds__(kThreads) plan_one_kernel(PlanArgs a) {
-  const bool ok = plan_sums(a);
+  __shared__ PlanWs head;
+  __shared__ int32_t sums[3 * kOneBlockSeqs + 2];
+  a.ws = &head;
+  a.old = sums;
+  a.need_sum = sums + a.t.B;
+  a.given_sum = a.need_sum + a.t.B + 1;
+  const bool ok = plan_sums<PER>(a);
   if (!ok) {
     for (int64_t r = threadIdx.x; r < a.T; r += kThreads) a.slots[r] = -1;
     return;
   }
-  const int given = a.ws->given, old_top = a.ws->old_top, top = a.ws->top;
-  for (int e = threadIdx.x; e < given; e += kThreads) plan_push(a, old_top, e);
+  const int old_top = a.ws->old_top, top = a.ws->top;
+  if (a.release)
+    for (int b = threadIdx.x >> 5; b < a.t.B; b += kThreads / 32)
+      plan_push(a, old_top, b, threadIdx.x & 31);
   __syncthreads();
-  for (int64_t r = threadIdx.x; r < a.T; r += kThreads) plan_row(a, top, r);
+  const int rows = a.offs[a.t.B];
+  for (int64_t r = threadIdx.x; r < a.T; r += kThreads) {
+    const int64_t row[1] = {r};
+    const int b[1] = {r < rows ? last_at_most(a.offs, a.t.B - 1, (int)r) : -1};
+    int64_t slot[1];
+    plan_rows<1>(a, top, row, b, slot);
+    a.slots[r] = slot[0];
+  }
+  for (int b = threadIdx.x; b < a.t.B; b += kThreads) plan_length(a, b);
 }
 
-__global__ void __launch_bounds__(kThreads) plan_sums_kernel(PlanArgs a) { plan_sums(a); }
+template <int PER>
+__global__ void __launch_bounds__(kThreads) plan_sums_kernel(PlanArgs a) {
+  plan_sums<PER>(a);
+}
+
+// (The kernels after the first are launched before it ends, and wait here.)
+__device__ __forceinline__ void wait_for_the_last_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 __global__ void __launch_bounds__(256) plan_push_kernel(PlanArgs a) {
-  if (!a.ws->ok) return;
-  const int given = a.ws->given, old_top = a.ws->old_top;
-  for (int e = blockIdx.x * 256 + threadIdx.x; e < given; e += gridDim.x * 256)
-    plan_push(a, old_top, e);
+  wait_for_the_last_kernel();
+  const int b = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (a.ws->ok && b < a.t.B) plan_push(a, a.ws->old_top, b, threadIdx.x & 31);
 }
 
+// 1024 rows a block: the first row's sequence by a search of 32 probes a step,
+// the others' among the 1024 that follow it, in shared memory.
+constexpr int kRowsBlock = 1024;
 __global__ void __launch_bounds__(256) plan_rows_kernel(PlanArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (row >= a.T) return;
-  if (!a.ws->ok) {
-    a.slots[row] = -1;
-    return;
+  __shared__ int first, win[kRowsBlock + 1];
+  wait_for_the_last_kernel();
+  const int64_t row0 = (int64_t)blockIdx.x * kRowsBlock + threadIdx.x;  // and 256, 512, 768 on
+  const bool ok = a.ws->ok;
+  const int top = a.ws->top, B = a.t.B, rows = a.offs[B];
+  const bool some = ok && row0 - threadIdx.x < rows;
+  if (some) {
+    if (threadIdx.x < 32) {
+      const int v = (int)(row0 - threadIdx.x);
+      int lo = 0, n = B;  // the sequence is among [lo, lo + n)
+      while (n > 1) {
+        const int step = (n + 31) / 32, p = lo + (int)threadIdx.x * step;
+        const uint32_t le = __ballot_sync(0xffffffffu, p < lo + n && a.offs[p] <= v);
+        const int k = 31 - __clz(le);  // (probe 0 always is)
+        n = imin(step, n - k * step);
+        lo += k * step;
+      }
+      if (threadIdx.x == 0) first = lo;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i <= kRowsBlock; i += 256) win[i] = a.offs[imin(first + i, B)];
+    __syncthreads();
   }
-  plan_row(a, a.ws->top, row);
+  constexpr int N = kRowsBlock / 256;
+  int64_t row[N], slot[N];
+  int b[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    row[i] = row0 + 256 * i;
+    b[i] = -1;
+    slot[i] = -1;
+    if (some && row[i] < rows)
+      b[i] = (int)row[i] < win[kRowsBlock]
+                 ? first + last_at_most(win, kRowsBlock - 1, (int)row[i])
+                 : last_at_most(a.offs, B - 1, (int)row[i]);
+  }
+  if (some) plan_rows<N>(a, top, row, b, slot);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (row[i] < a.T) a.slots[row[i]] = slot[i];
+    if (ok && row[i] < B) plan_length(a, (int)row[i]);
+  }
 }
 
 __global__ void __launch_bounds__(256)
@@ -234,12 +330,10 @@ __global__ void __launch_bounds__(256)
   slots[row] = slot;
 }
 
-// Rows up to which one block does the whole step.
-constexpr int64_t kOneBlockRows = 8192;
-
 }  // namespace
 
-size_t cache_plan_ws_bytes(int B) {
+size_t cache_plan_ws_bytes(int B, int64_t T) {
+  if (T <= kOneBlockRows && B <= kOneBlockSeqs) return 0;
   return align256(sizeof(PlanWs) + sizeof(int32_t) * (3 * (size_t)B + 2));
 }
 
@@ -257,14 +351,32 @@ cudaError_t launch_cache_plan(const CacheTab& t, const int32_t* offs, const int3
   a.old = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + sizeof(PlanWs));
   a.need_sum = a.old + t.B;
   a.given_sum = a.need_sum + t.B + 1;
-  if (T <= kOneBlockRows) {
-    plan_one_kernel<<<1, kThreads, 0, st>>>(a);
+  if (T <= kOneBlockRows && t.B <= kOneBlockSeqs) {
+    if (t.B <= kThreads) plan_one_kernel<1><<<1, kThreads, 0, st>>>(a);
+    else plan_one_kernel<4><<<1, kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
-  plan_sums_kernel<<<1, kThreads, 0, st>>>(a);
-  if (release) plan_push_kernel<<<148, 256, 0, st>>>(a);
-  plan_rows_kernel<<<(unsigned)((T + 255) / 256), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  if (t.B <= kThreads) plan_sums_kernel<1><<<1, kThreads, 0, st>>>(a);
+  else plan_sums_kernel<4><<<1, kThreads, 0, st>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && release) {
+    cfg.gridDim = dim3((unsigned)((t.B + 7) / 8));
+    e = cudaLaunchKernelEx(&cfg, plan_push_kernel, a);
+  }
+  if (e == cudaSuccess) {
+    const int64_t n = T > t.B ? T : t.B;  // a thread a row, and a thread a length
+    cfg.gridDim = dim3((unsigned)((n + kRowsBlock - 1) / kRowsBlock));
+    e = cudaLaunchKernelEx(&cfg, plan_rows_kernel, a);
+  }
+  return e;
 }
 
 cudaError_t launch_cache_slot_map(const CacheTab& t, const int32_t* offs, int64_t T,

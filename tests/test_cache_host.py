@@ -90,7 +90,7 @@ def _attend(**kw):
 
 
 BAD_TABLES = [("B", 0, _abi.ERR_INVALID_ARG), ("max_pages", 0, _abi.ERR_INVALID_ARG),
-              ("max_pages", (1 << 20) + 1, _abi.ERR_UNSUPPORTED),
+              ("max_pages", (1 << 19) + 1, _abi.ERR_UNSUPPORTED),
               ("num_pages", 0, _abi.ERR_INVALID_ARG), ("page_size", 48, _abi.ERR_UNSUPPORTED),
               ("page_size", 128, _abi.ERR_UNSUPPORTED), ("status", None, _abi.ERR_INVALID_ARG),
               ("lengths", FAKE + 2, _abi.ERR_INVALID_ARG),
@@ -111,17 +111,20 @@ def test_bad_tables_are_refused(lib, field, value, code):
 
 def test_plan_refusals(lib):
     t = _tables()
-    need = lib.hstu_cache_plan_workspace_bytes(4)
-    assert need >= 256 and need % 256 == 0 and lib.hstu_cache_plan_workspace_bytes(0) == 0
-    f = lib.hstu_cache_plan
-    assert f(None, FAKE, None, None, 10, FAKE, FAKE, need, None) == _abi.ERR_INVALID_ARG
-    assert f(t, None, None, None, 10, FAKE, FAKE, need, None) == _abi.ERR_INVALID_ARG
+    f, bytes_of = lib.hstu_cache_plan, lib.hstu_cache_plan_workspace_bytes
+    assert bytes_of(0, 10) == 0 and bytes_of(4, -1) == 0
+    assert bytes_of(4, 10) == 0  # a small step keeps its sums on chip
+    T = 100_000
+    need = bytes_of(4, T)
+    assert need >= 256 and need % 256 == 0 and bytes_of(5000, 1) > 0
+    assert f(None, FAKE, None, None, T, FAKE, FAKE, need, None) == _abi.ERR_INVALID_ARG
+    assert f(t, None, None, None, T, FAKE, FAKE, need, None) == _abi.ERR_INVALID_ARG
     assert f(t, FAKE, None, None, -1, FAKE, FAKE, need, None) == _abi.ERR_INVALID_ARG
-    assert f(t, FAKE, None, None, 10, FAKE + 4, FAKE, need, None) == _abi.ERR_INVALID_ARG
+    assert f(t, FAKE, None, None, T, FAKE + 4, FAKE, need, None) == _abi.ERR_INVALID_ARG
     assert f(t, FAKE, None, None, 1 << 31, FAKE, FAKE, need, None) == _abi.ERR_UNSUPPORTED
-    assert f(t, FAKE, None, None, 10, FAKE, None, need, None) == _abi.ERR_WORKSPACE
-    assert f(t, FAKE, None, None, 10, FAKE, FAKE + 128, need, None) == _abi.ERR_WORKSPACE
-    assert f(t, FAKE, None, None, 10, FAKE, FAKE, need - 1, None) == _abi.ERR_WORKSPACE
+    assert f(t, FAKE, None, None, T, FAKE, None, need, None) == _abi.ERR_WORKSPACE
+    assert f(t, FAKE, None, None, T, FAKE, FAKE + 128, need, None) == _abi.ERR_WORKSPACE
+    assert f(t, FAKE, None, None, T, FAKE, FAKE, need - 1, None) == _abi.ERR_WORKSPACE
 
 
 @pytest.mark.parametrize("field,value,code", [
