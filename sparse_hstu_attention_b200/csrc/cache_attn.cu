@@ -591,19 +591,26 @@ cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
 
 }  // namespace
 
-// Sequences of up to this many rows take the kernel above, longer ones tiles of
-// 128 rows on tcgen05.
-constexpr int kFewRows = 16;
+// Which kernel a call takes: the one above up to 32 rows a sequence, and up to 64
+// where its 8-row units do not even fill the GPU once; beyond that the tiles of
+// 128 rows on tcgen05.  Measured, above / tcgen05, us: 64 sequences x 4 heads of
+// 128 under a 512-token window 13 / 47 at 8 rows, 41 / 52 at 32, 73 / 52 at 64;
+// 24 x 8 of 32 under 256 tokens 18 / 29 at 32, 31 / 29 at 64; 4 x 4 of 64 7.2 /
+// 17.8 at 64; 1 x 4 of 128 over 16K tokens 35 / 45 at 64.
+bool few_rows(const CacheAttnArgs& a) {
+  const int64_t units = (int64_t)a.t.B * a.H * ((a.max_new + kRows - 1) / kRows);
+  return a.max_new <= 32 || (a.max_new <= 64 && units <= 2 * 148);
+}
 
 size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d) {
-  if (a.max_new > kFewRows) return cache_tc_ws_bytes(a, d);
+  if (!few_rows(a)) return cache_tc_ws_bytes(a, d);
   const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
   return p.S == 1 ? 0 : align256((size_t)p.units * p.S * kRows * d * sizeof(float));
 }
 
 cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st) {
   if (a.T == 0 || a.max_new == 0) return cudaSuccess;
-  if (a.max_new > kFewRows) return launch_cache_tc(a, d, ws, st);
+  if (!few_rows(a)) return launch_cache_tc(a, d, ws, st);
   float* parts = static_cast<float*>(ws);
   if (d == 32) return launch_step<32>(a, parts, st);
   if (d == 64) return launch_step<64>(a, parts, st);
