@@ -175,7 +175,11 @@ __device__ __forceinline__ void store_pair(const CacheAttnArgs& a, const CacheSe
 }
 
 // parts: fp32 [unit][S][8][D], the blocks' sums (S > 1 only).
-template <int D>
+// ONE: one row a unit.  All 8 columns of the scores then hold that row, so that
+// lane t of four takes only the tokens of score tile u = t, a quarter of the
+// pointwise work, and gives their P to column 2t of the second product; the
+// columns are added at the end.
+template <int D, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2)
     cache_step_kernel(const __grid_constant__ CacheAttnArgs a, int S, int row_tiles,
                       float* __restrict__ parts) {
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   CacheSeq sq;
   if (!cache_seq(a, b, &sq) || r0 >= sq.n || cache_status(a.t) != 0) return;
-  const int nr = imin(kRows, sq.n - r0);
+  const int nr = ONE ? 1 : imin(kRows, sq.n - r0);
   const CacheTiles tl = cache_tiles<kTK>(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
   const int bl = block_tiles(tl.n, S);
   const int e0 = imin(split * bl, tl.n), nt = imin(bl, tl.n - e0);  // this block's tiles
@@ -211,12 +215,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   // consumes tile k and then loads tile k + kStages into the stage it freed.
   // The first kStages tiles are loaded by the warps in turn, so a warp loads
   // tiles warp, warp + kW (if below kStages), then its own + kStages.
-  // Page ids of the tiles a warp consumes later are held 32 at a time, one per
-  // lane: entry i is tile kStages + warp + i kW.
+  // Page ids of what a warp loads are held 32 at a time, one a lane: its first
+  // two tiles', then those of the tiles it loads later, entry i ppt + p being page
+  // p of tile kStages + warp + i kW; the next 32 are read when the last are begun.
   const int32_t* bt = a.t.bt + (int64_t)b * a.t.M;
   const int pages = (sq.Lh + ps - 1) >> lps;
   auto page_id = [&](int k, int p) -> int {
-    if (k >= nt || p >= ppt) return 0;
+    if (k >= nt) return 0;
     const int i = tl.at(e0 + k) * ppt + p;
     if (i >= pages) return 0;
     const int x = bt[i];
@@ -224,36 +229,33 @@ __global__ void __launch_bounds__(kThreads, 2)
     cache_fail(a.t, HSTU_SLA_ERR_BAD_INPUT);
     return 0;
   };
-  auto load = [&](int k, const int (&id)[4]) {  // by one lane
+  const int lpp = 6 - lps;  // log2 of ppt
+  auto load = [&](int k, int ids, int at) {  // by the warp; ids: lanes at, at + 1, ...
+    const int id = __shfl_sync(0xffffffffu, ids, (at + lane) & 31);
     const uint32_t dst = ring + (k % kStages) * C::STG, bk = bar + 8 * (k % kStages);
     const int np = imin(ppt, pages - tl.at(e0 + k) * ppt);
-    mbar_expect_tx(bk, (uint32_t)(np * lay.bytes));
-    __threadfence_block();
-    gen[k % kStages] = k / kStages;
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-      if (p < np)
-        bulk_load(dst + p * pitch, a.pages + id[p] * a.page_stride + (int64_t)h * lay.bytes,
-                  (uint32_t)lay.bytes, bk);
+    if (lane == 0) {
+      mbar_expect_tx(bk, (uint32_t)(np * lay.bytes));
+      __threadfence_block();
+      gen[k % kStages] = k / kStages;
+    }
+    __syncwarp();
+    if (lane < np)
+      bulk_load(dst + lane * pitch, a.pages + id * a.page_stride + (int64_t)h * lay.bytes,
+                (uint32_t)lay.bytes, bk);
   };
   {
-    // lanes 0, 1: the warp's first loads; lane 2 on: entry lane - 2 would wait
-    int id[4];
-    const int k = warp + lane * kW;
-    const bool mine = k < kStages && k < nt;
-    if (mine) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p) id[p] = page_id(k, p);
-    }
+    const int k = warp + (lane >> lpp) * kW;  // lanes of tiles warp and warp + kW
+    const int id = k < kStages ? page_id(k, lane & (ppt - 1)) : 0;
     __syncthreads();  // barriers are initialised
-    if (mine) load(k, id);
+    if (warp < nt) load(warp, id, 0);
+    if (warp + kW < kStages && warp + kW < nt) load(warp + kW, id, ppt);
   }
-  int id[4];
-  auto load_ids = [&](int i0) {
-#pragma unroll
-    for (int p = 0; p < 4; ++p) id[p] = page_id(kStages + warp + (i0 + lane) * kW, p);
+  auto later_ids = [&](int i0) {
+    const int i = i0 + lane;
+    return page_id(kStages + warp + (i >> lpp) * kW, i & (ppt - 1));
   };
-  load_ids(0);
+  int ids = later_ids(0), ids_next = later_ids(32);
 
   // Q fragments of row g: this thread's quarter of its dims, in the order of a
   // K word's pairs, every second one divided by 16.  sum(q) alpha / 2, and the
@@ -264,11 +266,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t x[WD][4];
     uint32_t most = 0;
     float sum = 0.f;
-    const bf16* q0 = a.q + (int64_t)(sq.s0 + r0 + g) * a.q_rs + h * D + t * (D / 4);
+    const bf16* q0 = a.q + (int64_t)(sq.s0 + r0 + (ONE ? 0 : g)) * a.q_rs + h * D + t * (D / 4);
 #pragma unroll
     for (int w = 0; w < WD; ++w) {
       uint4 y = make_uint4(0, 0, 0, 0);
-      if (g < nr) y = *reinterpret_cast<const uint4*>(q0 + 8 * w);
+      if (ONE || g < nr) y = *reinterpret_cast<const uint4*>(q0 + 8 * w);
       x[w][0] = y.x; x[w][1] = y.y; x[w][2] = y.z; x[w][3] = y.w;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -300,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     f0 = __shfl_sync(0xffffffffu, f, 8 * t);
     f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
   }
-  const bool one = nr == 1;  // rows 2t + 1 do not exist
   const CacheRow cr0 = cache_row(r0 + imin(2 * t, nr - 1), sq.h, sq.Lh, a.K1, a.K2e);
   const CacheRow cr1 = cache_row(r0 + imin(2 * t + 1, nr - 1), sq.h, sq.Lh, a.K1, a.K2e);
   const CacheFull whole = cache_full(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
@@ -336,21 +337,49 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!ok) break;
     const int j0 = tl.at(e0 + k) * kTK;
     const uint32_t stg = ring + (k % kStages) * C::STG;
-    float p0[4][2], p1[4][2];  // P s of rows 2t, 2t + 1 at tokens j0 + jg + 4u (+ 2)
+    const bool full = whole(j0, kTK);
+    // P s of rows 2t, 2t + 1 at tokens j0 + jg + 4u (+ 2); ONE: of the row at u = t
+    constexpr int NU = ONE ? 1 : 4;
+    float p0[NU][2], p1[NU][2];
+    auto pointwise = [&](int u, int iu, const float (&st)[4]) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t kp[1], vp[1];
+        lds<1>(kp, stg + poff + 16 * u + 8 * e);
+        lds<1>(vp, stg + poff + (lay.vp - lay.kp) + 16 * u + 8 * e);
+        const float ks = bf_lo(kp[0]), km = bf_hi(kp[0]), vs = bf_lo(vp[0]), vm = bf_hi(vp[0]);
+        const int j = j0 + jg + 4 * u + 2 * e;
+        float x = fmaf(st[2 * e] * f0, ks, km * sum0);
+        float p = fmaf(x, tanh_approx(x), x), m = p * vm;
+        p0[iu][e] = p * vs;
+        if (!full) {
+          const bool see = j < cr0.pre || (j >= cr0.lo && j < cr0.hi);
+          p0[iu][e] = see ? p0[iu][e] : 0.f;
+          m = see ? m : 0.f;
+        }
+        rest0 += m;
+        p1[iu][e] = 0.f;
+        if constexpr (!ONE) {
+          x = fmaf(st[2 * e + 1] * f1, ks, km * sum1);
+          p = fmaf(x, tanh_approx(x), x);
+          m = p * vm;
+          p1[iu][e] = p * vs;
+          if (!full) {
+            const bool see = j < cr1.pre || (j >= cr1.lo && j < cr1.hi);
+            p1[iu][e] = see ? p1[iu][e] : 0.f;
+            m = see ? m : 0.f;
+          }
+          rest1 += m;
+        }
+      }
+    };
+    float mine[4] = {0.f, 0.f, 0.f, 0.f};  // ONE: the scores of u = t
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       float st[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t ka[WD], kb[WD], kp[2], vp[2];
+      uint32_t ka[WD], kb[WD];
       lds<WD>(ka, stg + koff + 4 * u * (D / 2));
       lds<WD>(kb, stg + koff + (4 * u + 2) * (D / 2));
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t x[1];
-        lds<1>(x, stg + poff + 16 * u + 8 * e);
-        kp[e] = x[0];
-        lds<1>(x, stg + poff + (lay.vp - lay.kp) + 16 * u + 8 * e);
-        vp[e] = x[0];
-      }
 #pragma unroll
       for (int w = 0; w < WD; ++w) {
         mma_f16(st, ka[w] & kLow, kb[w] & kLow, ka[w] & kHigh, kb[w] & kHigh, qf[2 * w][0],
@@ -359,56 +388,44 @@ __global__ void __launch_bounds__(kThreads, 2)
         mma_f16(st, x & kLow, y & kLow, x & kHigh, y & kHigh, qf[2 * w + 1][0],
                 qf[2 * w + 1][1]);
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float ks = bf_lo(kp[e]), km = bf_hi(kp[e]), vs = bf_lo(vp[e]), vm = bf_hi(vp[e]);
-        const int j = j0 + jg + 4 * u + 2 * e;
-        float x = fmaf(st[2 * e] * f0, ks, km * sum0);
-        float p = fmaf(x, tanh_approx(x), x), m = p * vm;
-        p0[u][e] = p * vs;
-        if (!whole(j0, kTK)) {
-          const bool see = j < cr0.pre || (j >= cr0.lo && j < cr0.hi);
-          p0[u][e] = see ? p0[u][e] : 0.f;
-          m = see ? m : 0.f;
-        }
-        rest0 += m;
-        p1[u][e] = 0.f;
-        if (!one) {
-          x = fmaf(st[2 * e + 1] * f1, ks, km * sum1);
-          p = fmaf(x, tanh_approx(x), x);
-          m = p * vm;
-          p1[u][e] = p * vs;
-          if (!whole(j0, kTK)) {
-            const bool see = j < cr1.pre || (j >= cr1.lo && j < cr1.hi);
-            p1[u][e] = see ? p1[u][e] : 0.f;
-            m = see ? m : 0.f;
-          }
-          rest1 += m;
-        }
+      if constexpr (ONE) {
+        mine[0] = u == t ? st[0] : mine[0];
+        mine[2] = u == t ? st[2] : mine[2];
+      } else {
+        pointwise(u, u, st);
       }
     }
+    if constexpr (ONE) pointwise(t, 0, mine);
     uint32_t pk[4][2];
     uint32_t big = 0;
+    auto pack = [&]() {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        pk[u][e] = pack_f16(p0[u][e] * sc0, p1[u][e] * sc1);
-        big = __vmaxu2(big, pk[u][e] & 0x7fff7fffu);
-      }
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (ONE) {
+            const uint32_t x = u == 0 ? pack_f16(p0[0][e] * sc0, 0.f) : pk[0][e];
+            pk[u][e] = x;
+          } else {
+            pk[u][e] = pack_f16(p0[u][e] * sc0, p1[u][e] * sc1);
+          }
+          if (!ONE || u == 0) big = __vmaxu2(big, pk[u][e] & 0x7fff7fffu);
+        }
+    };
+    pack();
     if (__any_sync(0xffffffffu, (big & 0xffffu) >= 0x7c00u || big >= 0x7c000000u)) {
       // P s beyond f16 with this scale (or the row's first): put its largest
       // into [2^4, 2^5)
       float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < NU; ++u)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           m0 = fmaxf(m0, fabsf(p0[u][e]));
           m1 = fmaxf(m1, fabsf(p1[u][e]));
         }
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) {
+      for (int x = ONE ? 1 : 4; x < 32; x <<= 1) {
         m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, x));
         m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, x));
       }
@@ -428,16 +445,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       sc0 = n0;
       sc1 = n1;
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) pk[u][e] = pack_f16(p0[u][e] * sc0, p1[u][e] * sc1);
+      pack();
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      pk[u][0] = transpose8x8(pk[u][0]);
-      pk[u][1] = transpose8x8(pk[u][1]);
-    }
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) pk[u][e] = transpose8x8(!ONE || u == t ? pk[u][e] : 0u);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       uint32_t vw[4];
@@ -450,12 +463,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     __syncwarp();
-    if (n_done > 0 && (n_done & 31) == 0) load_ids(n_done);
     if (k + kStages < nt) {
-      int x[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) x[p] = __shfl_sync(0xffffffffu, id[p], n_done & 31);
-      if (lane == 0) load(k + kStages, x);
+      const int at = n_done << lpp;
+      if (at > 0 && (at & 31) == 0) {
+        ids = ids_next;
+        ids_next = later_ids(at + 32);
+      }
+      load(k + kStages, ids, at & 31);
     }
   }
   // If a wait gave up, the copies in flight land before the ring is used again
@@ -469,8 +483,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   // The warp's result, [8][PITCH] fp32, and its rows' rest.
+  if constexpr (ONE) {
 #pragma unroll
-  for (int x = 4; x < 32; x <<= 1) {
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1) {
+        o[i][0] += __shfl_xor_sync(0xffffffffu, o[i][0], x);
+        o[i][2] += __shfl_xor_sync(0xffffffffu, o[i][2], x);
+      }
+  }
+#pragma unroll
+  for (int x = ONE ? 1 : 4; x < 32; x <<= 1) {
     rest0 += __shfl_xor_sync(0xffffffffu, rest0, x);
     rest1 += __shfl_xor_sync(0xffffffffu, rest1, x);
   }
@@ -577,13 +600,13 @@ int most_keys(const CacheAttnArgs& a) {
 template <int D>
 cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
   using C = StepCfg<D>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      cache_step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  auto kern = a.max_new == 1 ? cache_step_kernel<D, true> : cache_step_kernel<D, false>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
   if (p.units * p.S > 0x7fffffff) return cudaErrorInvalidValue;
-  cache_step_kernel<D><<<(unsigned)(p.units * p.S), kThreads, C::SMEM, st>>>(a, p.S, p.row_tiles,
-                                                                           parts);
+  kern<<<(unsigned)(p.units * p.S), kThreads, C::SMEM, st>>>(a, p.S, p.row_tiles, parts);
   if (p.S > 1)
     cache_join_kernel<D><<<(unsigned)p.units, kThreads, 0, st>>>(a, p.S, p.row_tiles, parts);
   return cudaGetLastError();
