@@ -542,6 +542,7 @@ __global__ void __launch_bounds__(kThreads)
     cache_join_kernel(const __grid_constant__ CacheAttnArgs a, int S, int row_tiles,
                       const float* __restrict__ parts) {
   __shared__ float self[kRows];
+  wait_for_the_last_kernel();
   const int unit = blockIdx.x, bh = unit / row_tiles, r0 = (unit % row_tiles) * kRows;
   const int b = bh / a.H, h = bh % a.H;
   CacheSeq sq;
@@ -567,8 +568,8 @@ __global__ void __launch_bounds__(kThreads)
 // Blocks a unit.  Two blocks fit an SM.  A unit is split until the GPU is full
 // once, and further, down to 8 tiles a warp, until it is full eight times, so
 // that the last blocks to finish cost little of the whole (64 sequences x 4
-// heads of 8K-16K tokens, d = 128: 103 us unsplit, 92 in 4, 102 in 8; 10-tile
-// windows of the same batch: 10.3 us unsplit, 16.5 in 2).
+// heads of 8K-16K tokens, d = 128, one row: 88 us unsplit, 81 in 4, 88 in 8;
+// 10-tile windows of the same batch: 9 us unsplit, 15 in 2).
 int step_splits(int64_t units, int64_t tiles) {
   const int64_t slots = 2 * 148;
   int64_t fill = (slots + units - 1) / units;
@@ -607,9 +608,10 @@ cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
   const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
   if (p.units * p.S > 0x7fffffff) return cudaErrorInvalidValue;
   kern<<<(unsigned)(p.units * p.S), kThreads, C::SMEM, st>>>(a, p.S, p.row_tiles, parts);
-  if (p.S > 1)
-    cache_join_kernel<D><<<(unsigned)p.units, kThreads, 0, st>>>(a, p.S, p.row_tiles, parts);
-  return cudaGetLastError();
+  const cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess || p.S == 1) return launched;
+  return launch_early(cache_join_kernel<D>, (unsigned)p.units, kThreads, st, a, p.S, p.row_tiles,
+                      (const float*)parts);
 }
 
 }  // namespace

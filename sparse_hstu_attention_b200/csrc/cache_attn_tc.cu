@@ -662,6 +662,7 @@ __global__ void __launch_bounds__(kThreads)
     cache_tc_join_kernel(const __grid_constant__ CacheAttnArgs a, int S, int row_tiles,
                          const float* __restrict__ parts) {
   constexpr int PL = D / 32;  // dims a lane
+  wait_for_the_last_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / 4, bh = unit / row_tiles, r0 = (unit % row_tiles) * kBM;
   const int b = bh / a.H, h = bh % a.H;
@@ -740,10 +741,10 @@ cudaError_t launch_tc(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
   if (p.units * p.S > 0x7fffffff || p.units * 4 > 0x7fffffff) return cudaErrorInvalidValue;
   cache_tc_kernel<D><<<(unsigned)(p.units * p.S), kThreads, C::SMEM, st>>>(a, p.S, p.row_tiles,
                                                                          parts);
-  if (p.S > 1)
-    cache_tc_join_kernel<D><<<(unsigned)(p.units * 4), kThreads, 0, st>>>(a, p.S, p.row_tiles,
-                                                                         parts);
-  return cudaGetLastError();
+  const cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess || p.S == 1) return launched;
+  return launch_early(cache_tc_join_kernel<D>, (unsigned)(p.units * 4), 256, st, a, p.S,
+                      p.row_tiles, (const float*)parts);
 }
 
 }  // namespace

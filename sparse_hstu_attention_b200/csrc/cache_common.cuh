@@ -155,6 +155,26 @@ __host__ __device__ __forceinline__ CacheFull cache_full(int r0, int r1, int h, 
   return f;
 }
 
+// A kernel launched by launch_early starts before the one ahead of it in the
+// stream has ended, and waits for that here.
+__device__ __forceinline__ void wait_for_the_last_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), unsigned grid, unsigned threads, cudaStream_t st,
+                         A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_cache_plan(const CacheTab& t, const int32_t* offs, const int32_t* nts,
                               const int32_t* release, int64_t T, int64_t* slots, void* ws,
                               cudaStream_t st);

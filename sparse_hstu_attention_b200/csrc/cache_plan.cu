@@ -248,11 +248,6 @@ __global__ void __launch_bounds__(kThreads) plan_sums_kernel(PlanArgs a) {
   plan_sums<PER>(a);
 }
 
-// (The kernels after the first are launched before it ends, and wait here.)
-__device__ __forceinline__ void wait_for_the_last_kernel() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __global__ void __launch_bounds__(256) plan_push_kernel(PlanArgs a) {
   wait_for_the_last_kernel();
   const int b = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -358,23 +353,12 @@ cudaError_t launch_cache_plan(const CacheTab& t, const int32_t* offs, const int3
   }
   if (t.B <= kThreads) plan_sums_kernel<1><<<1, kThreads, 0, st>>>(a);
   else plan_sums_kernel<4><<<1, kThreads, 0, st>>>(a);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && release) {
-    cfg.gridDim = dim3((unsigned)((t.B + 7) / 8));
-    e = cudaLaunchKernelEx(&cfg, plan_push_kernel, a);
-  }
+  if (e == cudaSuccess && release)
+    e = launch_early(plan_push_kernel, (unsigned)((t.B + 7) / 8), 256, st, a);
   if (e == cudaSuccess) {
     const int64_t n = T > t.B ? T : t.B;  // a thread a row, and a thread a length
-    cfg.gridDim = dim3((unsigned)((n + kRowsBlock - 1) / kRowsBlock));
-    e = cudaLaunchKernelEx(&cfg, plan_rows_kernel, a);
+    e = launch_early(plan_rows_kernel, (unsigned)((n + kRowsBlock - 1) / kRowsBlock), 256, st, a);
   }
   return e;
 }
