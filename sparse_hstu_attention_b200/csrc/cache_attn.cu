@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int bh = unit / row_tiles, r0 = (unit % row_tiles) * kRows;
   const int b = bh / a.H, h = bh % a.H;
 
+  const int status = cache_status(a.t);
   CacheSeq sq;
-  if (!cache_seq(a, b, &sq) || r0 >= sq.n || cache_status(a.t) != 0) return;
+  if (!cache_seq(a, b, &sq) || r0 >= sq.n) return;
   const int nr = ONE ? 1 : imin(kRows, sq.n - r0);
   const CacheTiles tl = cache_tiles<kTK>(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
   const int bl = block_tiles(tl.n, S);
@@ -247,7 +248,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   {
     const int k = warp + (lane >> lpp) * kW;  // lanes of tiles warp and warp + kW
     const int id = k < kStages ? page_id(k, lane & (ppt - 1)) : 0;
-    __syncthreads();  // barriers are initialised
+    // barriers are initialised; one status for the whole block, whose warps may
+    // have read different ones, so that they part ways together
+    if (__syncthreads_or(status != 0)) return;
     if (warp < nt) load(warp, id, 0);
     if (warp + kW < kStages && warp + kW < nt) load(warp + kW, id, ppt);
   }
@@ -546,12 +549,13 @@ __global__ void __launch_bounds__(kThreads)
   const int unit = blockIdx.x, bh = unit / row_tiles, r0 = (unit % row_tiles) * kRows;
   const int b = bh / a.H, h = bh % a.H;
   CacheSeq sq;
-  if (!cache_seq(a, b, &sq) || r0 >= sq.n || cache_status(a.t) != 0) return;
+  const int status = cache_status(a.t);
+  if (!cache_seq(a, b, &sq) || r0 >= sq.n) return;
   const int nr = imin(kRows, sq.n - r0);
   const CacheTiles tl = cache_tiles<kTK>(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
   const int used = imax(1, cdiv(tl.n, block_tiles(tl.n, S)));
   self_pairs<D>(a, sq, h, r0, nr, self);
-  __syncthreads();
+  if (__syncthreads_or(status != 0)) return;
   for (int e = threadIdx.x * 2; e < nr * D; e += 2 * kThreads) {
     const float* p = parts + (int64_t)unit * S * (kRows * D) + e;
     float2 x = make_float2(0.f, 0.f);

@@ -39,11 +39,14 @@ struct Groups {
   int heads[TT / 32 + 1];
 };
 
-// Slots of the tile's rows, checked; groups numbered.  Returns their count.
+// Slots of the tile's rows, checked; groups numbered.  Returns their count, or -1
+// if the tables' status is set: one answer for the whole block, whose warps may
+// read different ones while another block reports a bad slot.
 template <int TT>
 __device__ __forceinline__ int find_groups(const CacheRowArgs& a, int64_t t0, int head_off,
                                            Groups<TT>* g) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int status = cache_status(a.t);
   const int64_t n_slots = (int64_t)a.t.P << a.t.lps;
   if (tid < TT) {
     int64_t s = t0 + tid < a.T ? a.slots[t0 + tid] : -1;
@@ -56,7 +59,7 @@ __device__ __forceinline__ int find_groups(const CacheRowArgs& a, int64_t t0, in
     g->block[tid] = a.pages + (s < 0 ? 0 : s >> a.t.lps) * a.page_stride + head_off;
   }
   if (tid < Groups<TT>::kMost) g->mask[tid] = 0;
-  __syncthreads();
+  if (__syncthreads_or(status != 0)) return -1;
   int mine = 0;
   bool head = false;
   if (tid < TT) {
@@ -162,11 +165,11 @@ __global__ void __launch_bounds__(kThreads, 7) cache_append_kernel(CacheRowArgs 
   using G = Groups<TT>;
   __shared__ G g;
   __shared__ uint8_t sv[D / 2 * G::kPitch];
-  if (cache_status(a.t) != 0) return;
   const int64_t t0 = (int64_t)blockIdx.x * TT;
   const int h = blockIdx.y, ps = a.t.ps;
   const PageLayout<D> lay(ps);
   const int n_groups = find_groups<TT>(a, t0, h * lay.bytes, &g);
+  if (n_groups < 0) return;
   const bool grouped = n_groups <= G::kMost;
   const int w = threadIdx.x % LPR;
   const bf16* kp = a.k + (t0 + threadIdx.x / LPR) * a.k_rs + h * D + w * 8;
@@ -240,11 +243,11 @@ __global__ void __launch_bounds__(kThreads, 7) cache_read_kernel(CacheRowArgs a)
   using G = Groups<TT>;
   __shared__ G g;
   __shared__ uint8_t sv[D / 2 * G::kPitch];
-  if (cache_status(a.t) != 0) return;
   const int64_t t0 = (int64_t)blockIdx.x * TT;
   const int h = blockIdx.y, ps = a.t.ps;
   const PageLayout<D> lay(ps);
   const int n_groups = find_groups<TT>(a, t0, h * lay.bytes, &g);
+  if (n_groups < 0) return;
   const bool grouped = n_groups <= G::kMost;
   if (grouped) {
     for (int e = threadIdx.x; e < n_groups * (D / 2); e += kThreads) {

@@ -501,3 +501,212 @@ def test_long_histories(H, d, ps, B, most, rows):
         got, want, tol = run_attend(t, pages, tokens, lengths, [rows] * B, [0] * B, H, d, 3, K1=K1,
                                     K2=100, ctx=0, max_new=bound)
         check(got, want, tol)
+
+
+# ------------------------------------------------- what a server may also do
+KERNELS = [1, 70]  # rows a sequence: either attention kernel
+
+
+@pytest.mark.parametrize("rows", KERNELS + [9])
+@pytest.mark.parametrize("d", [32, 128])
+def test_rows_of_any_scale(rows, d):
+    """Rows of q from 2^-120 to 2^60, rows of zeros, and one that spans 2^20."""
+    H, ps, lengths = 2, 32, [333, 150]
+
+    def edit(q, k, v):
+        for t in range(q.shape[0]):
+            q[t, t % H] *= 2.0 ** (-120 + 60 * (t % 4))
+            if t % 5 == 3:
+                q[t, 1] = 0.0
+            if t % 7 == 2:
+                q[t, 0, ::2] *= 2.0 ** -20
+        q[-1, :] *= 2.0 ** 10
+
+    t, pages, tokens = filled(lengths, H, d, ps, 21)
+    for cand in ([0, 0], [rows, rows // 2]):
+        got, want, tol = run_attend(t, pages, tokens, lengths, [rows, rows], cand, H, d, 2, K1=200,
+                                    K2=40, ctx=0, max_new=rows, edit=edit)
+        check(got, want, tol)
+
+
+@pytest.mark.parametrize("rows", [3, 70])
+def test_a_row_that_is_not_finite_is_nan_alone(rows):
+    H, d, ps, lengths = 2, 64, 16, [200, 260]
+
+    def edit(q, k, v):
+        q[1, 0, 5], q[rows + 2, 1, 63] = float("nan"), float("inf")
+
+    t, pages, tokens = filled(lengths, H, d, ps, 22)
+    got, want, tol = run_attend(t, pages, tokens, lengths, [rows, rows], [0, 0], H, d, 2, K1=64,
+                                K2=0, ctx=0, max_new=rows, edit=edit)
+    for at, h in ((1, 0), (rows + 2, 1)):
+        assert bool(got[at, h].isnan().all())
+        got[at, h], want[at, h], tol[at, h] = 0, 0, 0
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("rows", KERNELS)
+def test_rows_without_a_range(rows):
+    """Keys and values that are constant along d have step 0 and are exact."""
+    H, d, ps, L = 1, 64, 16, 150
+    t, _ = tables_of([L], ps, 3)
+    pages = cache.allocate_pages(t.num_pages, H, d, ps, DEV)
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((L, H, 1), generator=g).bfloat16().expand(L, H, d).contiguous()
+            for _ in range(2))
+    cache.append(k.to(DEV), v.to(DEV), cache.slot_map(t, offs_of([L]), total_tokens=L), pages, t)
+    tokens = [tuple((c.double(), s, m) for c, s, m in (ref.quantise(k), ref.quantise(v)))]
+    assert all(not s.any() for _, s, _ in tokens[0])
+    got, want, tol = run_attend(t, pages, tokens, [L], [rows], [0], H, d, 4, K1=1 << 20, K2=0,
+                                ctx=0, max_new=rows)
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("lengths,rows,cand", [([40, 0, 9], [0, 0, 0], [0, 0, 0]),
+                                               ([500, 90], [2, 40], [0, 39]),
+                                               ([0, 0], [1, 90], [1, 90])])
+def test_no_bound_on_the_rows(lengths, rows, cand):
+    """max_new left out; steps without a row."""
+    t, pages, tokens = filled(lengths, 2, 32, 16, 23)
+    got, want, tol = run_attend(t, pages, tokens, lengths, rows, cand, 2, 32, 5, K1=90, K2=10,
+                                ctx=3, pad=5)
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("rows", KERNELS)
+def test_sequences_may_share_pages(rows):
+    """Several requests that read one user's pages."""
+    H, d, ps, L = 2, 128, 64, 700
+    t, pages, tokens = filled([L, L, L], H, d, ps, 24)
+    t.block_table[1:] = t.block_table[0]
+    got, want, tol = run_attend(t, pages, [tokens[0]] * 3, [L] * 3, [rows] * 3, [rows] * 3, H, d,
+                                6, K1=1 << 20, K2=0, ctx=0, max_new=rows)
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("rows", KERNELS)
+def test_rows_into_a_wider_tensor(rows):
+    """out as a column block: the other columns stay."""
+    H, d, ps, lengths = 2, 32, 32, [4000]
+    t, pages, _ = filled(lengths, H, d, ps, 25)
+    q, k, v = (x.to(DEV) for x in silu_rows(rows, H, d, 1))
+    kw = dict(contextual_len=0, K1=1 << 20, K2=0, alpha=0.2, N=50.0, max_new=rows)
+    want = cache.attend(q, None, None, offs_of([rows]), None, pages, t, **kw)
+    wide = torch.full((rows, 3 * H * d), 4.0, dtype=torch.bfloat16, device=DEV)
+    cache.attend(q, None, None, offs_of([rows]), None, pages, t,
+                 out=wide[:, H * d:2 * H * d].unflatten(1, (H, d)), **kw)
+    assert torch.equal(wide[:, H * d:2 * H * d].unflatten(1, (H, d)), want)
+    assert bool((wide[:, :H * d] == 4).all() and (wide[:, 2 * H * d:] == 4).all())
+
+
+def test_calls_on_a_given_stream():
+    """`stream` other than the current one, tensors released right behind the
+    calls: what the plain calls give."""
+    H, d, ps, lengths, rows = 2, 64, 32, [3000, 20], 70
+    t, pages, _ = filled(lengths, H, d, ps, 26)
+    t2 = cache.CacheTables(t.buf.clone(), t.B, t.max_pages, t.num_pages, ps)
+    p2 = pages.clone()
+    q, k, v = (x.to(DEV) for x in silu_rows(2 * rows, H, d, 1))
+    offs, nts = offs_of([rows, rows]), dev32([rows, rows - 1])
+    kw = dict(contextual_len=0, K1=1 << 20, K2=0, alpha=0.2, N=50.0, max_new=rows)
+
+    def step(t, pages, stream=None):
+        slots = cache.plan(t, offs, nts, total_tokens=2 * rows, stream=stream)
+        cache.append(k, v, slots, pages, t, stream=stream)
+        last = cache.slot_map(t, offs_of([7, 7]), total_tokens=14, stream=stream)
+        return (cache.attend(q, k, v, offs, nts, pages, t, stream=stream, **kw),
+                *cache.read(last, pages, t, stream=stream))
+
+    want = step(t, pages)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = step(t2, p2, s)
+    assert cache.get_error(t2, s) == 0
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+
+
+def test_two_graphs_at_once():
+    """Two captured calls over one cache, each with its own workspace, replayed
+    on two streams together."""
+    H, d, ps, lengths = 1, 128, 64, [6000]
+    t, pages, _ = filled(lengths, H, d, ps, 27)
+    runs = []
+    for rows in KERNELS + [200]:
+        q = silu_rows(rows, H, d, rows)[0].to(DEV)
+        offs = offs_of([rows])
+        kw = dict(contextual_len=0, K1=1 << 20, K2=0, alpha=0.2, N=50.0, max_new=rows)
+        want = cache.attend(q, None, None, offs, None, pages, t, **kw)
+        torch.cuda.synchronize()
+        s, graph, out = torch.cuda.Stream(), torch.cuda.CUDAGraph(), torch.empty_like(q)
+        with torch.cuda.stream(s):
+            graph.capture_begin()
+            cache.attend(q, None, None, offs, None, pages, t, out=out, **kw)
+            graph.capture_end()
+        runs.append((s, graph, out, want, q, offs))
+    for _ in range(20):
+        for _, _, out, *_ in runs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for s, graph, *_ in runs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, out, want, *_ in runs:
+            assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("what", ["first", "down", "past", "length", "page", "none"])
+def test_slot_map_reports_bad_inputs(what):
+    t, _ = tables_of([40, 0, 70], 16, 3)
+    offs, T = [0, 30, 30, 50], 50
+    if what == "first":
+        offs[0] = 1
+    if what == "down":
+        offs[1] = 20
+        offs[2] = 10
+    if what == "past":
+        offs[3] = 51
+    if what == "length":
+        t.lengths[2] = 19
+    if what == "page":
+        t.block_table[2, 3] = -1
+    if what == "none":  # no row at all, and offsets that say otherwise
+        T = 0
+    slots = cache.slot_map(t, dev32(offs), total_tokens=T)
+    assert slots.numel() == T and cache.get_error(t) == _abi.ERR_BAD_INPUT
+    assert bool(((slots >= -1) & (slots < t.num_pages * 16)).all())
+
+
+def test_many_blocks_that_report_at_once():
+    """Bad slots and pages all over a large call: the places no row names, and the
+    rows behind the last sequence, stay as they were, and the next plan starts
+    afresh."""
+    H, d, ps, B = 3, 64, 16, 40
+    lengths = [100 + b for b in range(B)]
+    t, pages, tokens = filled(lengths, H, d, ps, 28)
+    _, k, v = (x.to(DEV) for x in silu_rows(6000, H, d, 1))
+    keep = t.buf.clone()
+    for n in range(20):
+        before = pages.clone()
+        slots = torch.full((6000,), -1, dtype=torch.int64)
+        slots[n::3] = t.num_pages * ps + torch.arange(len(slots[n::3]))
+        free = int(t.free_pages[0])
+        slots[-1] = free * ps + 3  # a good one, in a page nobody has
+        cache.append(k, v, slots.to(DEV), pages, t)
+        assert cache.get_error(t) == _abi.ERR_BAD_INPUT
+        pages[free] = before[free]
+        assert torch.equal(pages, before)
+        t.buf.copy_(keep)
+        for rows in KERNELS:
+            t.block_table[n % 3::2, 2] = t.num_pages + 5
+            q = k[:B * rows + 9]
+            out = torch.full_like(q, 5.0)
+            cache.attend(q, None, None, offs_of([rows] * B), None, pages, t, contextual_len=0,
+                         K1=1 << 20, K2=0, alpha=0.1, N=9.0, max_new=rows, out=out)
+            assert cache.get_error(t) == _abi.ERR_BAD_INPUT
+            assert bool((out[B * rows:] == 5).all())
+            t.buf.copy_(keep)
+    got, want, tol = run_attend(t, pages, tokens, lengths, [1] * B, [0] * B, H, d, 3, K1=1 << 20,
+                                K2=0, ctx=0, max_new=1)
+    check(got, want, tol)
