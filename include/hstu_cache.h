@@ -102,8 +102,8 @@ int hstu_cache_plan(const hstu_cache_tables* t, const int32_t* seq_offsets,
 /* Slots of the last tokens of each sequence: row t of sequence b, the r-th of
  * its n_b = seq_offsets[b + 1] - seq_offsets[b] rows, is the token at position
  * lengths[b] - n_b + r; rows behind the last sequence get -1.  A sequence with
- * n_b > lengths[b], or offsets out of range, sets status
- * (HSTU_SLA_ERR_BAD_INPUT) and its rows get -1. */
+ * n_b > lengths[b], offsets, lengths or page ids out of range set status
+ * (HSTU_SLA_ERR_BAD_INPUT); the rows in question get -1, the others theirs or -1. */
 int hstu_cache_slot_map(const hstu_cache_tables* t, const int32_t* seq_offsets,
                         int64_t total_tokens, int64_t* slots, hstu_stream_t stream);
 
@@ -123,14 +123,16 @@ typedef struct {
   int64_t v_row_stride;
 } hstu_cache_rows;
 
-/* Quantise row t of k and v into slot slots[t].  A slot beyond the pages sets
- * status (HSTU_SLA_ERR_BAD_INPUT) and writes nothing.  Slots are distinct (two
- * rows of one slot leave either, or a mix). */
+/* Quantise row t of k and v into slot slots[t].  A row whose slot lies
+ * beyond the pages sets status (HSTU_SLA_ERR_BAD_INPUT) and is not written; the
+ * call's other rows then may or may not be.  Slots are distinct (two rows of one
+ * slot leave either, or a mix). */
 int hstu_cache_append(const hstu_cache_tables* t, const hstu_cache_rows* r,
                       hstu_stream_t stream);
 
 /* Row t of k and v becomes what slot slots[t] holds, m + s code rounded to
- * bf16, and zeros for a negative slot. */
+ * bf16, and zeros for a negative slot.  A slot beyond the pages sets status; what
+ * the call writes is then unspecified. */
 int hstu_cache_read(const hstu_cache_tables* t, const hstu_cache_rows* r, hstu_stream_t stream);
 
 /* SLA HSTU attention of the new rows over the cached histories.  After plan
@@ -146,9 +148,13 @@ int hstu_cache_read(const hstu_cache_tables* t, const hstu_cache_rows* r, hstu_s
  * What a row does not see does not reach it, whatever it holds: other
  * candidates' rows, masked tokens, the unused places of a page.
  *
+ * A row of q that holds a NaN or an infinity gives a NaN row (if it sees a key).
+ * Sums are held in fp32 and scaled inside by up to 2^24: finite inputs stay
+ * finite while |alpha| max|q| and the steps s are below 2^100 and the sums are.
+ *
  * A sequence whose offsets, targets, length or page ids are out of range, or
- * which has more than max_new rows, sets status (HSTU_SLA_ERR_BAD_INPUT); its
- * rows of out are then unspecified. */
+ * which has more than max_new rows, sets status (HSTU_SLA_ERR_BAD_INPUT); out's
+ * rows are then unspecified. */
 typedef struct {
   int32_t H;
   int32_t d;                   /* 32, 64 or 128 */

@@ -79,8 +79,9 @@ __device__ __forceinline__ int last_at_most(const int32_t* x, int n, int v) {
   return lo;
 }
 
-// The block's part: checks, sums and the new stack height.  All or nothing: the tables change only if every sequence's step can be done.
-// PER sequences a thread at a time, so that most batches take one scan.
+// The block's part: checks, sums and the new stack height.  All or nothing: the
+// tables change only if every sequence's step can be done.  PER sequences a thread
+// at a time, so that most batches take one scan.
 template <int PER>
 __device__ bool plan_sums(const PlanArgs& a) {
   __shared__ int sm[2][32];
@@ -302,25 +303,31 @@ __global__ void __launch_bounds__(256) plan_rows_kernel(PlanArgs a) {
   }
 }
 
+// A thread a row, and a thread a sequence's check.
 __global__ void __launch_bounds__(256)
     slot_map_kernel(CacheTab t, const int32_t* offs, int64_t T, int64_t* slots) {
   const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool on = cache_status(t) == 0;
+  if (on && row < t.B) {
+    const int b = (int)row, o0 = offs[b], o1 = offs[b + 1], len = t.lengths[b];
+    if ((b == 0 && o0 != 0) || o0 < 0 || o1 < o0 || (int64_t)o1 > T || len < 0 ||
+        len > t.M * t.ps || o1 - o0 > len)
+      cache_fail(t, HSTU_SLA_ERR_BAD_INPUT);
+  }
   if (row >= T) return;
   int64_t slot = -1;
-  if (cache_status(t) == 0 && row < offs[t.B] && offs[0] == 0) {
+  if (on && row < offs[t.B] && offs[0] == 0) {
     const int b = last_at_most(offs, t.B - 1, (int)row);
     const int n = offs[b + 1] - offs[b], r = (int)row - offs[b];
     const int len = t.lengths[b];
     const int pos = len - n + r;
-    bool ok = r >= 0 && r < n && n <= len && len <= t.M * t.ps;
-    if (ok) {
+    if (r >= 0 && r < n && n <= len && len <= t.M * t.ps) {
       const int page = t.bt[(int64_t)b * t.M + (pos >> t.lps)];
-      ok = page >= 0 && page < t.P;
-      slot = ok ? (int64_t)page * t.ps + (pos & (t.ps - 1)) : -1;
+      if (page >= 0 && page < t.P)
+        slot = (int64_t)page * t.ps + (pos & (t.ps - 1));
+      else
+        cache_fail(t, HSTU_SLA_ERR_BAD_INPUT);
     }
-    if (!ok) cache_fail(t, HSTU_SLA_ERR_BAD_INPUT);
-  } else if (row == 0 && offs[0] != 0) {
-    cache_fail(t, HSTU_SLA_ERR_BAD_INPUT);
   }
   slots[row] = slot;
 }
@@ -365,8 +372,8 @@ cudaError_t launch_cache_plan(const CacheTab& t, const int32_t* offs, const int3
 
 cudaError_t launch_cache_slot_map(const CacheTab& t, const int32_t* offs, int64_t T,
                                   int64_t* slots, cudaStream_t st) {
-  if (T == 0) return cudaSuccess;
-  slot_map_kernel<<<(unsigned)((T + 255) / 256), 256, 0, st>>>(t, offs, T, slots);
+  const int64_t n = T > t.B ? T : t.B;
+  slot_map_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(t, offs, T, slots);
   return cudaGetLastError();
 }
 
