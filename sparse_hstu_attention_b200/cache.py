@@ -182,7 +182,7 @@ def plan(tables: CacheTables, seq_offsets: torch.Tensor, num_targets: Optional[t
     o = _i32(seq_offsets, tables.B + 1, "seq_offsets", dev)
     nt = _i32(num_targets, tables.B, "num_targets", dev)
     rel = _i32(release, tables.B, "release", dev)
-    slots = _slots_out(slots, total_tokens, dev)
+    slots = _slots_out(slots, total_tokens, dev, stream)
     lib = _abi.load()
     ws = _workspace(workspace, lib.hstu_cache_plan_workspace_bytes(tables.B, total_tokens), dev,
                     stream)
@@ -193,24 +193,29 @@ def plan(tables: CacheTables, seq_offsets: torch.Tensor, num_targets: Optional[t
 
 
 def _workspace(workspace: Optional[torch.Tensor], need: int, dev, stream):
-    """The given workspace, checked, or a new one (kept from reuse until
-    `stream`, if another than the current one, is done with it); None if the call
-    needs none."""
+    """The given workspace, checked, or a new one; None if the call needs none."""
     if workspace is None:
         if need == 0:
             return None
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _new((need,), torch.uint8, dev, stream)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or \
             not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
     return workspace
 
 
-def _slots_out(slots, total_tokens, dev):
+def _new(shape, dtype, dev, stream) -> torch.Tensor:
+    """A tensor that a call allocates: kept from reuse until `stream`, if one is
+    given, is done with it."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _slots_out(slots, total_tokens, dev, stream):
     if slots is None:
-        return torch.empty(total_tokens, dtype=torch.int64, device=dev)
+        return _new((total_tokens,), torch.int64, dev, stream)
     _slots(slots, dev)
     if slots.numel() != total_tokens:
         raise ValueError(f"slots must have {total_tokens} elements")
@@ -229,7 +234,7 @@ def slot_map(tables: CacheTables, seq_offsets: torch.Tensor, *, total_tokens: in
     every sequence (e.g. to read whole histories back)."""
     dev = tables.device
     o = _i32(seq_offsets, tables.B + 1, "seq_offsets", dev)
-    slots = _slots_out(slots, total_tokens, dev)
+    slots = _slots_out(slots, total_tokens, dev, stream)
     _launch(dev, stream, "hstu_cache_slot_map", _abi.load().hstu_cache_slot_map, tables._c, o,
             total_tokens, slots.data_ptr())
     return slots
@@ -262,9 +267,9 @@ def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
     _slots(slots, dev)
     T = slots.numel()
     if k is None:
-        k = torch.empty(T, H, d, dtype=torch.bfloat16, device=dev)
+        k = _new((T, H, d), torch.bfloat16, dev, stream)
     if v is None:
-        v = torch.empty_like(k, memory_format=torch.contiguous_format)
+        v = _new((T, H, d), torch.bfloat16, dev, stream)
     r = _row_call(k, v, slots, pages, tables, H, d, stride)
     _launch(dev, stream, "hstu_cache_read", _abi.load().hstu_cache_read, tables._c, r)
     return k, v
@@ -293,7 +298,7 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
         k_rs, v_rs = _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev)
         k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _new((T, H, d), torch.bfloat16, dev, stream)
     p = _abi.CacheAttendParams(
         H, d, T, T if max_new is None else int(max_new),
         _i32(seq_offsets, tables.B + 1, "seq_offsets", dev),
@@ -308,7 +313,8 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
 
 
 def get_error(tables: CacheTables, stream=None) -> int:
-    """Synchronise and return the tables' status (0 = no error)."""
+    """Synchronise `stream` (default: the current one) and return the tables'
+    status (0 = no error)."""
     with torch.cuda.device(tables.device):
         return int(_abi.load().hstu_cache_get_error(tables._c,
                                                     _stream(stream, tables.device.index)))
