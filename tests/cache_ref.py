@@ -126,11 +126,12 @@ def attend(q, k, v, rows, cand, lengths, pages, *, K1, K2e, alpha, N):
 
     Bound, with P = SiLU(x), h = x / 2 and u = 2^-8 bf16's relative half step:
       u |out|            the result in bf16
-      u sum |P| s c      P s in bf16, the matrix product's operand
+      u sum |P| s c      P s in bf16 or f16, the matrix product's operand
       2^-10 sum |h| |v|  tanh's instruction (relative error below 2^-10.9)
-      1.1 dx |v|         x in fp32: sums of d products of q (16 + c) in d / 16
-                         matrix steps, each off by 2^-22 of the sum (SiLU' <= 1.1)
-      fp32 sums over n keys: n / 16 steps of P s (16 + c), and of P m."""
+      1.1 dx |v|         x in fp32: sums of d products of q c in d / 16 matrix
+                         steps, each off by 2^-22 of the sum (SiLU' <= 1.1); c
+                         taken as 31, the most a code with an offset of 16 is
+      fp32 sums over n keys: n / 16 steps of P s c (c as 31), and of P m."""
     out = torch.zeros(q.shape, dtype=torch.float64)
     tol = torch.zeros(q.shape, dtype=torch.float64)
     q, k, v = q.double(), k.double(), v.double()
