@@ -140,6 +140,26 @@ __device__ __forceinline__ bool phase_wait(uint32_t bar, uint32_t parity, const 
   return true;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(some ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(a)
+               : "memory");
+  return x;
+}
+
 // parts: fp32 [block][128][D], the blocks' sums (S > 1 only).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -211,20 +231,30 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto entry = [&](int n) -> const uint8_t* const* {
     return blocks + ((n / kIdTiles) & 1) * (kIdTiles * 8) + ((n % kIdTiles) << lpt);
   };
-  // q, and the candidates' k: D / 8 lanes a row, 16 rows a warp.
-  constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;
-  const int ch = lane % LPR, rw = warp * 16 + lane / LPR;
-  const bf16* const qp = a.q + (int64_t)(sq.s0 + r0 + rw) * a.q_rs + h * D + ch * 8;
-  const bf16* const kp = a.k + (int64_t)(sq.s0 + r0 + rw) * a.k_rs + h * D + ch * 8;
+  // The rows of q and the candidates' k as they are into the Q and K tiles, D / 8
+  // lanes a row; the candidates' v on its way to L2.
   const int cand = sq.h - r0;  // first candidate row of the block
-  uint4 q[IT], k[IT];
+  auto row_at = [&](int r, int c) -> uint32_t {  // 16-byte piece c of row r
+    const uint32_t sw = C::SWK == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
+    const int byte = 16 * c;
+    return byte / C::SWK * C::BOXK + r * C::SWK +
+           ((((uint32_t)(byte % C::SWK) >> 4) ^ sw) << 4);
+  };
+  {
+    constexpr int LPR = D / 8, RPI = 32 / LPR;
+    const int ch = lane % LPR, rw = warp * 16 + lane / LPR;
+    const int64_t row0 = sq.s0 + r0;
 #pragma unroll
-  for (int i = 0; i < IT; ++i) {
-    const int r = rw + i * RPI;
-    q[i] = k[i] = make_uint4(0, 0, 0, 0);
-    if (r < nr) q[i] = *reinterpret_cast<const uint4*>(qp + (int64_t)i * RPI * a.q_rs);
-    if (r < nr && r >= cand)
-      k[i] = *reinterpret_cast<const uint4*>(kp + (int64_t)i * RPI * a.k_rs);
+    for (int i = 0; i < 16 / RPI; ++i) {
+      const int r = rw + i * RPI;
+      const bool in = r < nr;
+      cp_async16(sQ + row_at(r, ch), in ? a.q + (row0 + r) * a.q_rs + h * D + ch * 8 : a.q, in);
+      if (in && r >= cand)
+        cp_async16(sK + row_at(r, ch), a.k + (row0 + r) * a.k_rs + h * D + ch * 8, true);
+    }
+    const int r = tid >> 1;
+    if (S == 1 && r >= cand && r < nr)
+      prefetch_l2(a.v + (row0 + r) * a.v_rs + h * D + (tid & 1) * (D / 2));
   }
   load_ids(0);
   tc_fence_before();
@@ -340,68 +370,60 @@ __global__ void __launch_bounds__(kThreads, 2)
     load_k(0);
     load_v(0);
   }
-  // q into shared memory (loaded above).
+  cp_async_wait();
+  __syncthreads();
+  // q into f16, in place: two lanes a row.
   bool common;
   {
-    // 16 bytes of f16 (q times up; the dims of high nibbles over 16) into row r
-    auto put = [&](int r, const uint4& y, float up) {
-      const uint32_t sw = C::SWK == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
-      const int byte = 16 * ch;
+    constexpr int NP = D / 16;  // pieces a lane
+    const int r = warp * 16 + (lane & 15), c0 = (lane >> 4) * NP;
+    // 16 bytes of f16: q times up; the dims of high nibbles over 16
+    auto put_q = [&](int c, const uint4& y, float up) {
       const float hi = up * 0.0625f;
-      st_shared_v4(sQ + byte / C::SWK * C::BOXK + r * C::SWK +
-                       ((((uint32_t)(byte % C::SWK) >> 4) ^ sw) << 4),
-                   pack_f16x2(bf_lo(y.x) * up, bf_hi(y.x) * up),
+      st_shared_v4(sQ + row_at(r, c), pack_f16x2(bf_lo(y.x) * up, bf_hi(y.x) * up),
                    pack_f16x2(bf_lo(y.y) * hi, bf_hi(y.y) * hi),
                    pack_f16x2(bf_lo(y.z) * up, bf_hi(y.z) * up),
                    pack_f16x2(bf_lo(y.w) * hi, bf_hi(y.w) * hi));
     };
-    bool fits = true;
-    float sum[IT], own[IT];
-    uint32_t most[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-      const uint32_t z[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
-      sum[i] = own[i] = 0.f;
-      most[i] = 0;
+    const bool is_cand = r >= cand && r < nr;
+    float sum = 0.f, own = 0.f;
+    uint32_t most = 0;
+#pragma unroll 4
+    for (int i = 0; i < NP; ++i) {
+      const uint4 q = ld_shared_v4(sQ + row_at(r, c0 + i));
+      uint4 k = make_uint4(0, 0, 0, 0);
+      if (is_cand) k = ld_shared_v4(sK + row_at(r, c0 + i));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w}, z[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sum[i] += bf_lo(w[j]) + bf_hi(w[j]);
-        own[i] = fmaf(bf_lo(w[j]), bf_lo(z[j]), fmaf(bf_hi(w[j]), bf_hi(z[j]), own[i]));
-        most[i] = umax(most[i], umax(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+        sum += bf_lo(w[j]) + bf_hi(w[j]);
+        own = fmaf(bf_lo(w[j]), bf_lo(z[j]), fmaf(bf_hi(w[j]), bf_hi(z[j]), own));
+        most = umax(most, umax(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
       }
-      put(rw + i * RPI, q[i], 16.f);
+      put_q(c0 + i, q, 16.f);
     }
-#pragma unroll
-    for (int o = 1; o < LPR; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-        own[i] += __shfl_xor_sync(0xffffffffu, own[i], o);
-        most[i] = umax(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
-      }
-    if (ch == 0) {
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int r = rw + i * RPI;
-        // most in [2^-6, 2^11), or a row of zeros: 2^4 will do; else the row's
-        // largest goes to [2^14, 2^15) (values below 2^-112: times 2^126)
-        fits = fits && (most[i] == 0 || (most[i] >= 121u << 7 && most[i] < 138u << 7));
-        const int e = imax((int)(most[i] >> 7) - 127, -112);
-        rd[r] = __int_as_float(imin(117 + e, 254) << 23);  // 2^(e - 10)
-        rd[128 + r] = most[i] >= 0x7f80u ? __int_as_float(0x7fc00000) : sum[i] * (0.5f * a.alpha);
-        const float y = own[i] * a.alpha;
-        rd[256 + r] = r >= cand ? __fdividef(y, 1.f + __expf(-y)) : 0.f;
-      }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    own += __shfl_xor_sync(0xffffffffu, own, 16);
+    most = umax(most, __shfl_xor_sync(0xffffffffu, most, 16));
+    // most in [2^-6, 2^11), or a row of zeros: 2^4 will do; else the row's largest
+    // goes to [2^14, 2^15) (values below 2^-112: times 2^126)
+    const bool fits = most == 0 || (most >= 121u << 7 && most < 138u << 7);
+    const int e = imax((int)(most >> 7) - 127, -112);
+    const float scale = __int_as_float(imin(117 + e, 254) << 23);  // 2^(e - 10)
+    if (lane < 16) {
+      rd[r] = scale;
+      rd[128 + r] = most >= 0x7f80u ? __int_as_float(0x7fc00000) : sum * (0.5f * a.alpha);
+      const float y = own * a.alpha;
+      rd[256 + r] = is_cand ? __fdividef(y, 1.f + __expf(-y)) : 0.f;
     }
     common = __syncthreads_and(fits);
     if (!common) {  // 2^(14 - e) for each row
+      const bf16* const qp = a.q + (int64_t)(sq.s0 + r0 + r) * a.q_rs + h * D;
 #pragma unroll 1
-      for (int i = 0; i < IT; ++i) {
-        const int r = rw + i * RPI;
+      for (int i = 0; i < NP; ++i) {
         uint4 y = make_uint4(0, 0, 0, 0);
-        if (r < nr) y = *reinterpret_cast<const uint4*>(qp + (int64_t)i * RPI * a.q_rs);
-        put(r, y, 16.f / rd[r]);
+        if (r < nr) y = *reinterpret_cast<const uint4*>(qp + 8 * (c0 + i));
+        put_q(c0 + i, y, 16.f / scale);
       }
     }
   }
@@ -440,7 +462,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   // half, those 2t, 2t + 1 of each eight.
   const int quad = warp & 3, chalf = warp >> 2;
   const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-  const CacheFull whole = cache_full(r0, r0 + nr, sq.h, sq.Lh, a.K1, a.K2e);
+  // rows [q0, q1) are this warp's
+  const int q0 = r0 + quad * 32, q1 = imin(q0 + 32, r0 + nr);
+  const CacheFull whole = cache_full(q0, q1, sq.h, sq.Lh, a.K1, a.K2e);
   uint64_t rest[4] = {0, 0, 0, 0};  // packed pairs of fp32 sums of P m'
   bool ok = true;
 
@@ -475,64 +499,80 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int j0 = tl.at(e0 + n) * kBN;
       const ulonglong2* par =
           reinterpret_cast<const ulonglong2*>(sm + C::OFF_PAR + (n & 1) * 2048) + chalf * 64;
-      // FAST: every pair visible, one factor for all rows (in the steps s)
-      auto pointwise = [&](auto fast) {
+      // 16 columns.  FAST: every pair visible, one factor for all rows (in the steps s)
+      auto piece = [&](auto fast, int cg) {
         constexpr bool FAST = decltype(fast)::value;
-#pragma unroll 2
-        for (int cg = 0; cg < 4; ++cg) {  // 16 columns each
-          const uint32_t at = lanes + kColS + chalf * 64 + cg * 16;
-          uint32_t s0[8], s1[8];
-          tmem_ld_frag(at, s0);
-          tmem_ld_frag(at + (16u << 16), s1);
-          tmem_ld_frag_wait(s0, s1);
-          uint32_t bits[4];
-          float f[4];
-          if constexpr (!FAST) {
-            // this thread's columns of the 16, per row
-            const int jc = j0 + chalf * 64 + cg * 16;
+        const uint32_t at = lanes + kColS + chalf * 64 + cg * 16;
+        uint32_t s0[8], s1[8];
+        tmem_ld_frag(at, s0);
+        tmem_ld_frag(at + (16u << 16), s1);
+        tmem_ld_frag_wait(s0, s1);
+        uint32_t bits[4];
+        float f[4];
+        if constexpr (!FAST) {
+          // this thread's columns of the 16, per row
+          const int jc = j0 + chalf * 64 + cg * 16;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const CacheRow c = cache_row(r0 + imin(quad * 32 + g + 8 * i, nr - 1), sq.h,
-                                           sq.Lh, a.K1, a.K2e);
-              bits[i] = (range_bits(0, c.pre, jc) | range_bits(c.lo, c.hi, jc)) >> (2 * t);
-              f[i] = common ? 1.f : rd[quad * 32 + g + 8 * i];
-            }
+          for (int i = 0; i < 4; ++i) {
+            const CacheRow c = cache_row(imin(q0 + g + 8 * i, q1 - 1), sq.h, sq.Lh, a.K1, a.K2e);
+            bits[i] = (range_bits(0, c.pre, jc) | range_bits(c.lo, c.hi, jc)) >> (2 * t);
+            f[i] = common ? 1.f : rd[quad * 32 + g + 8 * i];
           }
-          uint32_t p0[4], p1[4];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {  // 8 columns each
-            const ulonglong2 kp = par[(cg * 8 + 4 * i + t) * 2];      // s s, m m
-            const ulonglong2 vp = par[(cg * 8 + 4 * i + t) * 2 + 1];  // of V
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint32_t* s = (r < 2 ? s0 : s1) + 4 * i + 2 * (r & 1);
-              uint64_t y = f2(s[0], s[1]);
-              if constexpr (!FAST) y = f2_mul(y, f2s(f[r]));
-              y = f2_fma(y, kp.x, f2_mul(kp.y, qs[r]));
-              const uint64_t p = f2_fma(y, f2_tanh(y), y);
-              uint32_t pv = f2_bf16(f2_mul(p, vp.x));
-              if constexpr (FAST) {
-                rest[r] = f2_fma(p, vp.y, rest[r]);
-              } else {
-                const bool a0 = bits[r] >> (8 * i) & 1u, a1 = bits[r] >> (8 * i + 1) & 1u;
-                pv &= (a0 ? 0xffffu : 0u) | (a1 ? 0xffff0000u : 0u);
-                const uint64_t pm = f2_mul(p, vp.y);
-                rest[r] = f2_add(rest[r], f2(a0 ? (uint32_t)pm : 0u,
-                                             a1 ? (uint32_t)(pm >> 32) : 0u));
-              }
-              (r < 2 ? p0 : p1)[2 * i + (r & 1)] = pv;
-            }
-          }
-          // P of columns [32 c, 32 c + 32) in columns [32 c, 32 c + 16)
-          const uint32_t to = lanes + kColS + chalf * 64 + (cg >> 1) * 32 + (cg & 1) * 8;
-          tmem_st_frag(to, p0);
-          tmem_st_frag(to + (16u << 16), p1);
         }
+        uint32_t p0[4], p1[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // 8 columns each
+          const ulonglong2 kp = par[(cg * 8 + 4 * i + t) * 2];      // s s, m m
+          const ulonglong2 vp = par[(cg * 8 + 4 * i + t) * 2 + 1];  // of V
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t* s = (r < 2 ? s0 : s1) + 4 * i + 2 * (r & 1);
+            uint64_t y = f2(s[0], s[1]);
+            if constexpr (!FAST) y = f2_mul(y, f2s(f[r]));
+            y = f2_fma(y, kp.x, f2_mul(kp.y, qs[r]));
+            const uint64_t p = f2_fma(y, f2_tanh(y), y);
+            uint32_t pv = f2_bf16(f2_mul(p, vp.x));
+            if constexpr (FAST) {
+              rest[r] = f2_fma(p, vp.y, rest[r]);
+            } else {
+              const bool a0 = bits[r] >> (8 * i) & 1u, a1 = bits[r] >> (8 * i + 1) & 1u;
+              pv &= (a0 ? 0xffffu : 0u) | (a1 ? 0xffff0000u : 0u);
+              const uint64_t pm = f2_mul(p, vp.y);
+              rest[r] = f2_add(rest[r],
+                               f2(a0 ? (uint32_t)pm : 0u, a1 ? (uint32_t)(pm >> 32) : 0u));
+            }
+            (r < 2 ? p0 : p1)[2 * i + (r & 1)] = pv;
+          }
+        }
+        // P of columns [32 c, 32 c + 32) in columns [32 c, 32 c + 16)
+        const uint32_t to = lanes + kColS + chalf * 64 + (cg >> 1) * 32 + (cg & 1) * 8;
+        tmem_st_frag(to, p0);
+        tmem_st_frag(to + (16u << 16), p1);
       };
-      if (common && whole(j0, kBN))
-        pointwise(std::true_type{});
-      else
-        pointwise(std::false_type{});
+      const int jw = j0 + chalf * 64;  // the warp's columns
+      if (common && q0 < q1 && whole(jw, 64)) {
+#pragma unroll 2
+        for (int cg = 0; cg < 4; ++cg) piece(std::true_type{}, cg);
+      } else {
+        // an edge of the masks (or rows of differing scales): pieces that no row of
+        // the warp sees are zeros
+        const CacheRow lo = cache_row(q0, sq.h, sq.Lh, a.K1, a.K2e);
+        const CacheRow hi = cache_row(q1 - 1, sq.h, sq.Lh, a.K1, a.K2e);
+#pragma unroll 1
+        for (int cg = 0; cg < 4; ++cg) {
+          const int jc = jw + cg * 16;
+          if (q0 >= q1 || (jc >= hi.pre && (jc + 16 <= lo.lo || jc >= hi.hi))) {
+            const uint32_t zero[4] = {0, 0, 0, 0};
+            const uint32_t to = lanes + kColS + chalf * 64 + (cg >> 1) * 32 + (cg & 1) * 8;
+            tmem_st_frag(to, zero);
+            tmem_st_frag(to + (16u << 16), zero);
+          } else if (common && whole(jc, 16)) {
+            piece(std::true_type{}, cg);
+          } else {
+            piece(std::false_type{}, cg);
+          }
+        }
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncthreads();
@@ -721,16 +761,24 @@ struct TcPlan {
   int64_t units;
 };
 
-// Two blocks fit an SM; a unit is split until they are all taken, down to two
-// tiles a block.
+// Two blocks fit an SM.  A unit is split while all its parts still run at once, down
+// to two tiles each, and further, down to 16 tiles each, until there are half as many
+// again, which evens out histories of differing lengths (4 x 4 heads x 8 row tiles
+// over up to 128 key tiles: 262 us unsplit, 178 in 2, 136 in 3, 126 in 4, 135 in 5).
+// Units of few tiles stay whole (64 x 4 x 4 row tiles over 5 key tiles: 105 us, 203
+// in 2).
 TcPlan tc_plan(const CacheAttnArgs& a) {
   TcPlan p;
   p.row_tiles = (a.max_new + kBM - 1) / kBM;
   p.units = (int64_t)a.t.B * a.H * p.row_tiles;
   const int64_t w = (int64_t)a.K1 + a.K2e + kBM, c = (int64_t)a.t.M * a.t.ps;
   const int64_t tiles = (w < c ? w : c) / kBN + 2;
-  int64_t S = p.units > 0 ? (2 * 148 + p.units - 1) / p.units : 1;
-  S = S < tiles / 2 ? S : tiles / 2;
+  const int64_t slots = 2 * 148, n = p.units > 0 ? p.units : 1;
+  int64_t fill = slots / n;
+  fill = fill < tiles / 2 ? fill : tiles / 2;
+  int64_t even = (slots * 3 / 2 + n - 1) / n;
+  even = even < tiles / 16 ? even : tiles / 16;
+  const int64_t S = fill > even ? fill : even;
   p.S = S < 1 ? 1 : (int)S;
   return p;
 }
