@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const CacheFull whole = cache_full(q0, q1, sq.h, sq.Lh, a.K1, a.K2e);
   uint64_t rest[4] = {0, 0, 0, 0};  // packed pairs of fp32 sums of P m'
   bool ok = true;
+  int n = 0;
 
   if (nt > 0) {
     store_k(0);
@@ -477,7 +478,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t qs[4] = {f2s(rd[128 + quad * 32 + g]), f2s(rd[128 + quad * 32 + g + 8]),
                             f2s(rd[128 + quad * 32 + g + 16]),
                             f2s(rd[128 + quad * 32 + g + 24])};
-    int n = 0;
     for (; n < nt; ++n) {
       // V of this tile, once the last tile's product has read its own
       if (n > 0) ok = phase_wait(bar_o, (n - 1) & 1, a.t);
@@ -584,13 +584,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (warp == 0) issue_s();
       }
     }
-    // the last product; if a wait gave up, whatever was issued
-    if (ok) {
-      ok = phase_wait(bar_o, (nt - 1) & 1, a.t);
-    } else {
-      drain_wait(bar_s, n & 1);
-      if (n > 0) drain_wait(bar_o, (n - 1) & 1);
-    }
+  }
+  // The candidates' v (see below): all loads before the first use.
+  constexpr int NA = D >= 64 ? 2 : 1, NC = D == 128 ? 2 : 1;
+  uint4 vv[NA * NC][2];
+#pragma unroll
+  for (int i = 0; i < NA * NC * 2; ++i) {
+    const int la = D >= 64 ? (i >> 1) / NC : chalf;
+    const int c0 = D >= 64 ? (chalf * NC + (i >> 1) % NC) * 32 : 0;
+    const int r = quad * 32 + 16 * la + 8 * (i & 1) + g;
+    vv[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+    if (S == 1 && r >= cand && r < nr)
+      vv[i >> 1][i & 1] = *reinterpret_cast<const uint4*>(
+          a.v + (int64_t)(sq.s0 + r0 + r) * a.v_rs + h * D + c0 + 8 * t);
   }
   // rests: a row's four lanes, then the two column halves
 #pragma unroll
@@ -599,6 +605,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     x += __shfl_xor_sync(0xffffffffu, x, 2);
     if (t == 0) rests[chalf * 128 + quad * 32 + g + 8 * r] = x;
+  }
+  // the last product; if a wait gave up, whatever was issued
+  if (nt > 0) {
+    if (ok) {
+      ok = phase_wait(bar_o, (nt - 1) & 1, a.t);
+    } else {
+      drain_wait(bar_s, n & 1);
+      if (n > 0) drain_wait(bar_o, (n - 1) & 1);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -609,19 +624,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // instruction).  A warp has its quarter's rows and half of the dims, at d = 32
   // half of the rows.
   {
-    constexpr int NA = D >= 64 ? 2 : 1, NC = D == 128 ? 2 : 1;
     const int64_t row0 = sq.s0 + r0;
-    uint4 vv[NA * NC][2];  // the candidates' v: all loads before the first use
-#pragma unroll
-    for (int i = 0; i < NA * NC * 2; ++i) {
-      const int la = D >= 64 ? (i >> 1) / NC : chalf;
-      const int c0 = D >= 64 ? (chalf * NC + (i >> 1) % NC) * 32 : 0;
-      const int r = quad * 32 + 16 * la + 8 * (i & 1) + g;
-      vv[i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
-      if (S == 1 && r >= cand && r < nr)
-        vv[i >> 1][i & 1] =
-            *reinterpret_cast<const uint4*>(a.v + (row0 + r) * a.v_rs + h * D + c0 + 8 * t);
-    }
 #pragma unroll
     for (int ac = 0; ac < NA * NC; ++ac) {
       const int la = D >= 64 ? ac / NC : chalf;                 // 16 lanes of the quarter
