@@ -622,15 +622,18 @@ cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
 
 }  // namespace
 
-// Which kernel a call takes: the one above up to 32 rows a sequence, and up to 64
-// where its 8-row units do not even fill the GPU once; beyond that the tiles of
-// 128 rows on tcgen05.  Measured, above / tcgen05, us: 64 sequences x 4 heads of
-// 128 under a 512-token window 13 / 47 at 8 rows, 41 / 52 at 32, 73 / 52 at 64;
-// 24 x 8 of 32 under 256 tokens 18 / 29 at 32, 31 / 29 at 64; 4 x 4 of 64 7.2 /
-// 17.8 at 64; 1 x 4 of 128 over 16K tokens 35 / 45 at 64.
+// Which kernel a call takes: the one above up to 16 rows a sequence, and while its
+// 8-row units fit the GPU at once up to 64 (32 if there are more than 4096 keys);
+// beyond that the tiles of 128 rows on tcgen05.  Measured, above / tcgen05, us:
+//   64 sequences x 4 heads of 128, 512-token window: 12 / 23 at 4 rows, 23 / 23 at 16,
+//   39 / 24 at 32; 24 x 8 of 32, 256 tokens: 12 / 13 at 16, 17 / 14 at 32;
+//   9 x 4 of 128, 512 tokens: 10 / 18 at 32, 13 / 18 at 64; over 8K tokens 33 / 35 at
+//   16, 43 / 39 at 32, 66 / 41 at 64; 16 x 4 of 128 over 16K: 98 / 124 at 24, 114 /
+//   127 at 32.
 bool few_rows(const CacheAttnArgs& a) {
   const int64_t units = (int64_t)a.t.B * a.H * ((a.max_new + kRows - 1) / kRows);
-  return a.max_new <= 32 || (a.max_new <= 64 && units <= 2 * 148);
+  return a.max_new <= 16 ||
+         (units <= 2 * 148 && a.max_new <= (most_keys(a) <= 4096 ? 64 : 32));
 }
 
 size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d) {
