@@ -37,9 +37,9 @@
 // dim pair) are then single 16-byte loads, without bank conflicts.
 //
 // Bound: HBM for long histories (d + 8 bytes per token and head); instructions
-// come next.  64 sequences x 4 heads of 128 over 8K-16K tokens, one row: 81 us,
-// 5.2 TB/s.  Under a window of 512 tokens the same batch takes 9.4 us, and one
-// sequence of 300 tokens 4.4: the latency of table, page id, page and products.
+// come next.  64 sequences x 4 heads of 128 over 8K-16K tokens, one row: 80 us,
+// 5.2 TB/s.  Under a window of 512 tokens the same batch takes 9.0 us, and one
+// sequence of 300 tokens 4.3: the latency of table, page id, page and products.
 #include <cuda_fp16.h>
 
 #include "cache_common.cuh"

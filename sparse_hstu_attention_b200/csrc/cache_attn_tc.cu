@@ -28,15 +28,20 @@
 // tiles (V transposed: its bytes lie along the tokens).  Scores are read from
 // TMEM as 16 x 256-bit fragments: a thread has 4 rows and a quarter of the
 // columns, so the per-key pairs are one 16-byte load per two columns and four
-// rows.  The loop over 16-column pieces is unrolled by two only: the code of a
-// kernel that unrolls everything outgrows the instruction cache.
+// rows.  The loop over 16-column pieces is unrolled by two: by four it is 3% quicker
+// at d = 64, 1% slower at d = 128 and spills there; rolled up, 1 to 4% slower.
 //
-// Bound: issue slots, some 5850 warp instructions a 128 x 128 tile at d = 128
-// (half of them on the scores, a third on unpacking), of which 65% are used: 2400
-// clocks a tile and SM.  The special-function unit (one tanh a score, 1024 clocks
-// a tile) and the products (as long) come behind.  64 sequences x 4 heads x 512
-// candidates under a 512-token window: 109 us; 4 x 4 x 1000 over up to 16K tokens:
-// 134 us; 16 x 8 heads of 64, 716 rows over a 1024-token window: 84 us.
+// Tiles at an edge of the masks are done in 16-column pieces of 32 rows each: whole
+// ones as inside, ones that no row sees as zeros, and only the others with masks (700
+// rows over a 1024-token window: 84 us without, 74 so).
+//
+// Bound: latency and issue slots.  A 128 x 128 tile takes some 5500 warp instructions
+// at d = 128, half of them on the scores and a third on unpacking, and 1.52 us of an
+// SM (48% of the slots; 1.2 us at d = 64); the special-function unit's part (one tanh
+// a score) is 0.55 us, the products' as long.  Two blocks of 8 warps with 128
+// registers are what an SM holds.  64 sequences x 4 heads x 512 candidates under a
+// 512-token window: 94 us; 4 x 4 x 1000 over up to 16K tokens: 124 us; 16 x 8 heads of
+// 64, 716 rows over a 1024-token window: 74 us.
 #include <type_traits>
 
 #include "cache_common.cuh"
