@@ -197,17 +197,16 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, dev, stream):
     if workspace is None:
         if need == 0:
             return None
-        workspace = _new((need,), torch.uint8, dev, stream)
+        workspace = _made(torch.empty(need, dtype=torch.uint8, device=dev), stream)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or \
             not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
     return workspace
 
 
-def _new(shape, dtype, dev, stream) -> torch.Tensor:
+def _made(t: torch.Tensor, stream) -> torch.Tensor:
     """A tensor that a call allocates: kept from reuse until `stream`, if one is
     given, is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -215,7 +214,7 @@ def _new(shape, dtype, dev, stream) -> torch.Tensor:
 
 def _slots_out(slots, total_tokens, dev, stream):
     if slots is None:
-        return _new((total_tokens,), torch.int64, dev, stream)
+        return _made(torch.empty(total_tokens, dtype=torch.int64, device=dev), stream)
     _slots(slots, dev)
     if slots.numel() != total_tokens:
         raise ValueError(f"slots must have {total_tokens} elements")
@@ -267,9 +266,9 @@ def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
     _slots(slots, dev)
     T = slots.numel()
     if k is None:
-        k = _new((T, H, d), torch.bfloat16, dev, stream)
+        k = _made(torch.empty(T, H, d, dtype=torch.bfloat16, device=dev), stream)
     if v is None:
-        v = _new((T, H, d), torch.bfloat16, dev, stream)
+        v = _made(torch.empty_like(k, memory_format=torch.contiguous_format), stream)
     r = _row_call(k, v, slots, pages, tables, H, d, stride)
     _launch(dev, stream, "hstu_cache_read", _abi.load().hstu_cache_read, tables._c, r)
     return k, v
@@ -298,7 +297,7 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
         k_rs, v_rs = _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev)
         k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
     if out is None:
-        out = _new((T, H, d), torch.bfloat16, dev, stream)
+        out = _made(torch.empty_like(q, memory_format=torch.contiguous_format), stream)
     p = _abi.CacheAttendParams(
         H, d, T, T if max_new is None else int(max_new),
         _i32(seq_offsets, tables.B + 1, "seq_offsets", dev),
