@@ -4,6 +4,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libhstu_sla.so")
@@ -142,6 +143,11 @@ class CacheAttendParams(ctypes.Structure):
     ]
 
 
+# The two as bytes, for calls of some microseconds: packing takes a third of a
+# Structure's time, and refuses what does not fit a field.
+CACHE_ROWS = struct.Struct("@iiqPPqPPqq")
+CACHE_ATTEND = struct.Struct("@iiqiPPiiiffPPPqqqPqPq")
+
 _lib = None
 
 
@@ -228,6 +234,12 @@ def load():
     lib.hstu_cache_attend.restype = ctypes.c_int
     lib.hstu_cache_get_error.argtypes = [tab, vp]
     lib.hstu_cache_get_error.restype = ctypes.c_int
+    # the calls with packed bytes in the struct's place
+    for name in ("hstu_cache_append", "hstu_cache_read", "hstu_cache_attend",
+                 "hstu_cache_attend_workspace_bytes"):
+        f, g = lib[name], getattr(lib, name)
+        f.argtypes, f.restype = [tab, vp] + g.argtypes[2:], g.restype
+        setattr(lib, name + "_packed", f)
     _lib = lib
     return lib
 

@@ -25,7 +25,7 @@ in the same tensors: nothing about them is read on the host.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -57,6 +57,8 @@ class CacheTables:
             raise TypeError("buf must be a contiguous CUDA int32 tensor")
         if B < 1 or max_pages < 1 or num_pages < 1:
             raise ValueError("B, max_pages and num_pages must be at least 1")
+        if page_size not in (16, 32, 64) or max(B, max_pages, num_pages) >= 1 << 31:
+            raise ValueError("page_size must be 16, 32 or 64, the sizes below 2^31")
         n = self.words(B, max_pages, num_pages)
         if buf.numel() < n:
             raise ValueError(f"buf has {buf.numel()} words, needs {n}")
@@ -239,11 +241,11 @@ def slot_map(tables: CacheTables, seq_offsets: torch.Tensor, *, total_tokens: in
     return slots
 
 
-def _row_call(k, v, slots, pages, tables, H, d, page_stride):
-    dev = tables.device
-    T = slots.numel()
-    return _abi.CacheRows(H, d, T, slots.data_ptr(), pages.data_ptr(), page_stride, k.data_ptr(),
-                          v.data_ptr(), _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev))
+def _pack(layout: struct.Struct, *values) -> bytes:
+    try:
+        return layout.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"an argument is out of range ({e})") from None
 
 
 def append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pages: torch.Tensor,
@@ -253,8 +255,11 @@ def append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pages: torch.T
     H, d, stride = _pages(pages, tables)
     dev = tables.device
     _slots(slots, dev)
-    r = _row_call(k, v, slots, pages, tables, H, d, stride)
-    _launch(dev, stream, "hstu_cache_append", _abi.load().hstu_cache_append, tables._c, r)
+    T = slots.numel()
+    k_rs, v_rs = _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev)
+    r = _pack(_abi.CACHE_ROWS, H, d, T, slots.data_ptr(), pages.data_ptr(), stride, k.data_ptr(),
+              v.data_ptr(), k_rs, v_rs)
+    _launch(dev, stream, "hstu_cache_append", _abi.load().hstu_cache_append_packed, tables._c, r)
 
 
 def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
@@ -265,12 +270,18 @@ def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
     dev = tables.device
     _slots(slots, dev)
     T = slots.numel()
+    k_rs = v_rs = H * d
     if k is None:
         k = _made(torch.empty(T, H, d, dtype=torch.bfloat16, device=dev), stream)
+    else:
+        k_rs = _rows(k, "k", T, H, d, dev)
     if v is None:
-        v = _made(torch.empty_like(k, memory_format=torch.contiguous_format), stream)
-    r = _row_call(k, v, slots, pages, tables, H, d, stride)
-    _launch(dev, stream, "hstu_cache_read", _abi.load().hstu_cache_read, tables._c, r)
+        v = _made(torch.empty(T, H, d, dtype=torch.bfloat16, device=dev), stream)
+    else:
+        v_rs = _rows(v, "v", T, H, d, dev)
+    r = _pack(_abi.CACHE_ROWS, H, d, T, slots.data_ptr(), pages.data_ptr(), stride, k.data_ptr(),
+              v.data_ptr(), k_rs, v_rs)
+    _launch(dev, stream, "hstu_cache_read", _abi.load().hstu_cache_read_packed, tables._c, r)
     return k, v
 
 
@@ -289,24 +300,26 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
     dev = tables.device
     T = q.shape[0]
     q_rs = _rows(q, "q", T, H, d, dev)
-    k_ptr = v_ptr = None
-    k_rs = v_rs = 0
+    k_ptr = v_ptr = k_rs = v_rs = 0
     if num_targets is not None:
         if k is None or v is None:
             raise ValueError("candidates (num_targets) need their rows of k and v")
         k_rs, v_rs = _rows(k, "k", T, H, d, dev), _rows(v, "v", T, H, d, dev)
         k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
+    o_rs = H * d
     if out is None:
         out = _made(torch.empty_like(q, memory_format=torch.contiguous_format), stream)
-    p = _abi.CacheAttendParams(
-        H, d, T, T if max_new is None else int(max_new),
-        _i32(seq_offsets, tables.B + 1, "seq_offsets", dev),
-        _i32(num_targets, tables.B, "num_targets", dev), int(contextual_len), int(K1), int(K2),
-        float(alpha), float(N), q.data_ptr(), k_ptr, v_ptr, q_rs, k_rs, v_rs, pages.data_ptr(),
-        stride, out.data_ptr(), _rows(out, "out", T, H, d, dev))
+    else:
+        o_rs = _rows(out, "out", T, H, d, dev)
+    p = _pack(_abi.CACHE_ATTEND, H, d, T, T if max_new is None else int(max_new),
+              _i32(seq_offsets, tables.B + 1, "seq_offsets", dev),
+              _i32(num_targets, tables.B, "num_targets", dev) or 0, int(contextual_len), int(K1),
+              int(K2), alpha, N, q.data_ptr(), k_ptr, v_ptr, q_rs, k_rs, v_rs, pages.data_ptr(),
+              stride, out.data_ptr(), o_rs)
     lib = _abi.load()
-    ws = _workspace(workspace, lib.hstu_cache_attend_workspace_bytes(tables._c, p), dev, stream)
-    _launch(dev, stream, "hstu_cache_attend", lib.hstu_cache_attend, tables._c, p,
+    ws = _workspace(workspace, lib.hstu_cache_attend_workspace_bytes_packed(tables._c, p), dev,
+                    stream)
+    _launch(dev, stream, "hstu_cache_attend", lib.hstu_cache_attend_packed, tables._c, p,
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return out
 

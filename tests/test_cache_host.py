@@ -191,3 +191,24 @@ def test_tables_refuse_wrong_buffers():
     assert n == 64 + 64 + 64 + 15
     with pytest.raises(TypeError):
         cache.CacheTables(torch.zeros(n, dtype=torch.int32), 3, 5, 7, 64)  # not on a GPU
+
+
+def test_packed_arguments_have_the_structs_layout():
+    """CACHE_ROWS and CACHE_ATTEND place every field where the ctypes structs do."""
+    for layout, struct_ in ((_abi.CACHE_ROWS, _abi.CacheRows),
+                            (_abi.CACHE_ATTEND, _abi.CacheAttendParams)):
+        values = [0.5 * i if t is ctypes.c_float else 3 * i + 1
+                  for i, (_, t) in enumerate(struct_._fields_)]
+        s = struct_.from_buffer_copy(layout.pack(*values))
+        assert ctypes.sizeof(struct_) == layout.size
+        assert [getattr(s, n) for n, _ in struct_._fields_] == values
+
+
+def test_arguments_beyond_their_fields_are_refused():
+    """A window of 2^40 is refused, not taken modulo 2^32."""
+    ok = [4, 128, 10, 10, FAKE, 0, 0, 8, 4, 0.1, 10.0, FAKE, FAKE, FAKE, 512, 512, 512, FAKE, 64,
+          FAKE, 512]
+    assert len(cache._pack(_abi.CACHE_ATTEND, *ok)) == ctypes.sizeof(_abi.CacheAttendParams)
+    for at, value in ((3, 1 << 31), (6, -1 << 40), (7, 1 << 32), (8, 1 << 40), (9, 10 ** 400)):
+        with pytest.raises(ValueError):
+            cache._pack(_abi.CACHE_ATTEND, *ok[:at], value, *ok[at + 1:])

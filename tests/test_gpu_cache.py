@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import cache_ref as ref
-from sparse_hstu_attention_b200 import _abi, cache
+from sparse_hstu_attention_b200 import SLAError, _abi, cache
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -710,3 +710,18 @@ def test_many_blocks_that_report_at_once():
     got, want, tol = run_attend(t, pages, tokens, lengths, [1] * B, [0] * B, H, d, 3, K1=1 << 20,
                                 K2=0, ctx=0, max_new=1)
     check(got, want, tol)
+
+
+def test_sizes_beyond_their_fields_are_refused():
+    t, pages, _ = filled([20], 2, 32, 16, 1)
+    q = silu_rows(2, 2, 32, 0)[0].to(DEV)
+    kw = dict(contextual_len=0, K1=4, K2=0, alpha=0.1, N=1.0)
+    for name, value in (("K1", 1 << 32), ("K2", 1 << 40), ("contextual_len", 1 << 31),
+                        ("max_new", 1 << 33), ("alpha", 1e300), ("N", -1.0)):
+        # (a float that fp32 lacks is an infinity, which the library refuses)
+        with pytest.raises(SLAError if name in ("alpha", "N") else ValueError):
+            cache.attend(q, None, None, offs_of([2]), None, pages, t, **{**kw, name: value})
+    for bad in (dict(B=1 << 31), dict(num_pages=1 << 32), dict(page_size=16 + (1 << 32)),
+                dict(page_size=48)):
+        with pytest.raises(ValueError):
+            cache.CacheTables(t.buf, **{**dict(B=1, max_pages=2, num_pages=3, page_size=16), **bad})
