@@ -62,7 +62,7 @@ extern "C" {
  *   block_table  [B][max_pages] page of a sequence's tokens
  *                [i page_size, (i + 1) page_size) at entry i */
 typedef struct {
-  int32_t B;          /* >= 1 */
+  int32_t B;          /* 1 .. 2^30 */
   int32_t max_pages;  /* per sequence, 1 .. 2^19 */
   int32_t num_pages;  /* >= 1 */
   int32_t page_size;  /* 16, 32 or 64 */
@@ -154,7 +154,8 @@ int hstu_cache_read(const hstu_cache_tables* t, const hstu_cache_rows* r, hstu_s
  *
  * A sequence whose offsets, targets, length or page ids are out of range, or
  * which has more than max_new rows, sets status (HSTU_SLA_ERR_BAD_INPUT); out's
- * rows are then unspecified. */
+ * rows are then unspecified.  2^29 blocks (B H times max_new in 128s, or in 8s for
+ * few rows) are the most there can be: beyond, HSTU_SLA_ERR_UNSUPPORTED. */
 typedef struct {
   int32_t H;
   int32_t d;                   /* 32, 64 or 128 */

@@ -20,7 +20,7 @@ int make_tab(const hstu_cache_tables* t, CacheTab* c) {
   if (t->page_size != 16 && t->page_size != 32 && t->page_size != 64)
     return HSTU_SLA_ERR_UNSUPPORTED;
   if (t->B < 1 || t->num_pages < 1 || t->max_pages < 1) return HSTU_SLA_ERR_INVALID_ARG;
-  if (t->max_pages > (1 << 19)) return HSTU_SLA_ERR_UNSUPPORTED;
+  if (t->max_pages > (1 << 19) || t->B > (1 << 30)) return HSTU_SLA_ERR_UNSUPPORTED;
   const void* ptrs[] = {t->status, t->free_count, t->lengths, t->free_pages, t->block_table};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned(p, 4)) return HSTU_SLA_ERR_INVALID_ARG;
@@ -120,7 +120,12 @@ int attend_args(const hstu_cache_tables* t, const hstu_cache_attend_params* p, C
   return HSTU_SLA_OK;
 }
 
-int status_of(cudaError_t e) { return e == cudaSuccess ? HSTU_SLA_OK : HSTU_SLA_ERR_CUDA; }
+// (cudaErrorNotSupported: the launch's own, more blocks than a grid has)
+int status_of(cudaError_t e) {
+  return e == cudaSuccess             ? HSTU_SLA_OK
+         : e == cudaErrorNotSupported ? HSTU_SLA_ERR_UNSUPPORTED
+                                      : HSTU_SLA_ERR_CUDA;
+}
 
 }  // namespace
 

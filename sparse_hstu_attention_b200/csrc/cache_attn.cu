@@ -590,13 +590,6 @@ struct StepPlan {
   int row_tiles, S;
   int64_t units;
 };
-StepPlan step_plan(int B, int H, int max_new, int max_keys) {
-  StepPlan p;
-  p.row_tiles = (max_new + kRows - 1) / kRows;
-  p.units = (int64_t)B * H * p.row_tiles;
-  p.S = p.units > 0 ? step_splits(p.units, max_keys / kTK + 2) : 1;
-  return p;
-}
 
 // Most keys a row tile can meet.
 int most_keys(const CacheAttnArgs& a) {
@@ -604,15 +597,23 @@ int most_keys(const CacheAttnArgs& a) {
   return (int)(w < c ? w : c);
 }
 
+StepPlan step_plan(const CacheAttnArgs& a) {
+  StepPlan p;
+  p.row_tiles = (int)((a.max_new + (int64_t)kRows - 1) / kRows);
+  p.units = cache_units(a, kRows);
+  p.S = p.units > 0 ? step_splits(p.units, most_keys(a) / kTK + 2) : 1;
+  return p;
+}
+
 template <int D>
 cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
   using C = StepCfg<D>;
   auto kern = a.max_new == 1 ? cache_step_kernel<D, true> : cache_step_kernel<D, false>;
+  const StepPlan p = step_plan(a);
+  if (p.units * p.S > 0x7fffffff) return cudaErrorNotSupported;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
-  if (p.units * p.S > 0x7fffffff) return cudaErrorInvalidValue;
   kern<<<(unsigned)(p.units * p.S), kThreads, C::SMEM, st>>>(a, p.S, p.row_tiles, parts);
   const cudaError_t launched = cudaGetLastError();
   if (launched != cudaSuccess || p.S == 1) return launched;
@@ -631,14 +632,14 @@ cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
 //   16, 43 / 39 at 32, 66 / 41 at 64; 16 x 4 of 128 over 16K: 98 / 124 at 24, 114 /
 //   127 at 32.
 bool few_rows(const CacheAttnArgs& a) {
-  const int64_t units = (int64_t)a.t.B * a.H * ((a.max_new + kRows - 1) / kRows);
+  const int64_t units = cache_units(a, kRows);
   return a.max_new <= 16 ||
          (units <= 2 * 148 && a.max_new <= (most_keys(a) <= 4096 ? 64 : 32));
 }
 
 size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d) {
   if (!few_rows(a)) return cache_tc_ws_bytes(a, d);
-  const StepPlan p = step_plan(a.t.B, a.H, a.max_new, most_keys(a));
+  const StepPlan p = step_plan(a);
   return p.S == 1 ? 0 : align256((size_t)p.units * p.S * kRows * d * sizeof(float));
 }
 

@@ -777,8 +777,8 @@ struct TcPlan {
 // in 2).
 TcPlan tc_plan(const CacheAttnArgs& a) {
   TcPlan p;
-  p.row_tiles = (a.max_new + kBM - 1) / kBM;
-  p.units = (int64_t)a.t.B * a.H * p.row_tiles;
+  p.row_tiles = (int)((a.max_new + (int64_t)kBM - 1) / kBM);
+  p.units = cache_units(a, kBM);
   const int64_t w = (int64_t)a.K1 + a.K2e + kBM, c = (int64_t)a.t.M * a.t.ps;
   const int64_t tiles = (w < c ? w : c) / kBN + 2;
   const int64_t slots = 2 * 148, n = p.units > 0 ? p.units : 1;
@@ -794,11 +794,11 @@ TcPlan tc_plan(const CacheAttnArgs& a) {
 template <int D>
 cudaError_t launch_tc(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
   using C = TcCfg<D>;
+  const TcPlan p = tc_plan(a);
+  if (p.units > 0x7fffffff / 4 / p.S) return cudaErrorNotSupported;
   const cudaError_t e = cudaFuncSetAttribute(
       cache_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const TcPlan p = tc_plan(a);
-  if (p.units * p.S > 0x7fffffff || p.units * 4 > 0x7fffffff) return cudaErrorInvalidValue;
   cache_tc_kernel<D><<<(unsigned)(p.units * p.S), kThreads, C::SMEM, st>>>(a, p.S, p.row_tiles,
                                                                          parts);
   const cudaError_t launched = cudaGetLastError();

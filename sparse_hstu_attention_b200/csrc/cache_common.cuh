@@ -175,6 +175,13 @@ cudaError_t launch_early(void (*kern)(P...), unsigned grid, unsigned threads, cu
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Units of a call: B H row tiles (held where it stays beyond any grid, and within 64
+// bits).
+inline int64_t cache_units(const CacheAttnArgs& a, int rows) {
+  const int64_t bh = (int64_t)a.t.B * a.H, most = (int64_t)1 << 33;
+  return (bh < most ? bh : most) * ((a.max_new + (int64_t)rows - 1) / rows);
+}
+
 cudaError_t launch_cache_plan(const CacheTab& t, const int32_t* offs, const int32_t* nts,
                               const int32_t* release, int64_t T, int64_t* slots, void* ws,
                               cudaStream_t st);

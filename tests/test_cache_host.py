@@ -212,3 +212,15 @@ def test_arguments_beyond_their_fields_are_refused():
     for at, value in ((3, 1 << 31), (6, -1 << 40), (7, 1 << 32), (8, 1 << 40), (9, 10 ** 400)):
         with pytest.raises(ValueError):
             cache._pack(_abi.CACHE_ATTEND, *ok[:at], value, *ok[at + 1:])
+
+
+@pytest.mark.parametrize("max_new,total", [(1, 10), (16, 1 << 20), (1 << 20, 1 << 20),
+                                           ((1 << 31) - 1, (1 << 31) - 1)])
+def test_more_blocks_than_a_grid_are_refused(lib, max_new, total):
+    t = _tables(B=1 << 30)
+    p = _attend(max_new=max_new, total_tokens=total, H=65535, page_stride=65535 * 64 * 136,
+                **{k: 65535 * 128 for k in ("q_row_stride", "k_row_stride", "v_row_stride",
+                                            "out_row_stride")})
+    assert lib.hstu_cache_attend(t, p, FAKE, 1 << 60, None) == _abi.ERR_UNSUPPORTED
+    assert lib.hstu_cache_attend(_tables(B=(1 << 30) + 1), p, FAKE, 1 << 60,
+                                 None) == _abi.ERR_UNSUPPORTED
