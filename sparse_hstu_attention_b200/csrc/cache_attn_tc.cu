@@ -214,28 +214,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int32_t* const bt = a.t.bt + (int64_t)b * a.t.M;
   const uint8_t* const head = a.pages + (int64_t)h * lay.bytes;
 
-  // This head's block of the pages of tiles [32 c, 32 c + 32).  Places past the
-  // cached tokens get page 0's: what is read there is masked.
-  auto load_ids = [&](int c) {
+  // This head's block of the pages of tiles [32 c, 32 c + 32), an entry a thread: its
+  // id, and its address into the table.  Places past the cached tokens get page 0's:
+  // what is read there is masked.
+  auto read_id = [&](int c) -> int {
     const int n = c * kIdTiles + (tid >> lpt);
+    if (tid >= kIdTiles << lpt || n >= nt) return 0;
+    const int i = (tl.at(e0 + n) << lpt) + (tid & ((1 << lpt) - 1));
+    return i < pages ? bt[i] : 0;
+  };
+  auto put_id = [&](int c, int id) {
     if (tid >= kIdTiles << lpt) return;
-    const uint8_t* p = head;
-    if (n < nt) {
-      const int i = (tl.at(e0 + n) << lpt) + (tid & ((1 << lpt) - 1));
-      if (i < pages) {
-        const int id = bt[i];
-        if (id >= 0 && id < a.t.P)
-          p = head + id * a.page_stride;
-        else
-          cache_fail(a.t, HSTU_SLA_ERR_BAD_INPUT);
-      }
+    if (id < 0 || id >= a.t.P) {
+      cache_fail(a.t, HSTU_SLA_ERR_BAD_INPUT);
+      id = 0;
     }
-    blocks[(c & 1) * (kIdTiles * 8) + tid] = p;
+    blocks[(c & 1) * (kIdTiles * 8) + tid] = head + id * a.page_stride;
   };
   // Table entry of the first page of tile n.
   auto entry = [&](int n) -> const uint8_t* const* {
     return blocks + ((n / kIdTiles) & 1) * (kIdTiles * 8) + ((n % kIdTiles) << lpt);
   };
+  const int id0 = read_id(0);
   // The rows of q and the candidates' k as they are into the Q and K tiles, D / 8
   // lanes a row; the candidates' v on its way to L2.
   const int cand = sq.h - r0;  // first candidate row of the block
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (S == 1 && r >= cand && r < nr)
       prefetch_l2(a.v + (row0 + r) * a.v_rs + h * D + (tid & 1) * (D / 2));
   }
-  load_ids(0);
+  put_id(0, id0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           load_k(n + 1);
           load_v(n + 1);
         }
-        if ((n & (kIdTiles - 1)) == 8 && n + kIdTiles - 8 < nt) load_ids(n / kIdTiles + 1);
+        if ((n & (kIdTiles - 1)) == 8 && n + kIdTiles - 8 < nt)
+          put_id(n / kIdTiles + 1, read_id(n / kIdTiles + 1));
         ok = phase_wait(bar_s, n & 1, a.t);
       }
       if (!__syncthreads_and(ok)) {
