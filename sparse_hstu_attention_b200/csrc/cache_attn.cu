@@ -63,8 +63,8 @@ struct StepCfg {
   static constexpr int OFF_REST = kStages * STG;    // [warp][8]
   static constexpr int OFF_SELF = OFF_REST + kW * kRows * 4;
   static constexpr int OFF_BAR = OFF_SELF + kRows * 4;
-  static constexpr int OFF_GEN = OFF_BAR + kStages * 8;  // phase a stage is armed for
-  static constexpr int SMEM = OFF_GEN + kStages * 4;
+  static constexpr int OFF_ARMED = OFF_BAR + kStages * 8;  // phase a stage is armed for
+  static constexpr int SMEM = OFF_ARMED + kStages * 4;
   static_assert(kStages * STG >= kW * kRows * PITCH * 4, "the warps' results fit the ring");
 };
 
@@ -90,11 +90,12 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, cons
   return true;
 }
 
-// Waits, as long at most, until *gen is n.
-__device__ __forceinline__ bool bounded_armed(const volatile int* gen, int n, const CacheTab& t) {
-  if (*gen == n) return true;
+// Waits, as long at most, until tile k's stage is armed for it.
+__device__ __forceinline__ bool bounded_armed(const volatile int* armed, int k,
+                                              const CacheTab& t) {
+  if (ring_armed(armed, k, kStages)) return true;
   const uint64_t t0 = globaltimer();
-  while (*gen != n) {
+  while (!ring_armed(armed, k, kStages)) {
     if (globaltimer() - t0 > kWaitLimitNs) {
       cache_fail(t, HSTU_SLA_ERR_TIMEOUT);
       return false;
@@ -207,8 +208,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const PageLayout<D> lay(ps);
   const int pitch = lay.bytes + (ps < kTK ? 2 * ps : 0);
   const uint32_t ring = smem_addr(smem), bar = ring + C::OFF_BAR;
-  volatile int* gen = reinterpret_cast<volatile int*>(smem + C::OFF_GEN);
+  volatile int* armed = reinterpret_cast<volatile int*>(smem + C::OFF_ARMED);
   if (threadIdx.x == 0) {
+    ring_clear(armed, kStages);
     for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
     fence_barrier_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       mbar_expect_tx(bk, (uint32_t)(np * lay.bytes));
       __threadfence_block();
-      gen[k % kStages] = k / kStages;
+      ring_arm(armed, k, kStages);
     }
     __syncwarp();
     if (lane < np)
@@ -250,8 +252,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   {
     const int k = warp + (lane >> lpp) * kW;  // lanes of tiles warp and warp + kW
     const int id = k < kStages ? page_id(k, lane & (ppt - 1)) : 0;
-    // barriers are initialised; one status for the whole block, whose warps may
-    // have read different ones, so that they part ways together
+    // barriers and phase words are initialised; one status for the whole block, whose
+    // warps may have read different ones, so that they part ways together
     if (__syncthreads_or(status != 0)) return;
     if (warp < nt) load(warp, id, 0);
     if (warp + kW < kStages && warp + kW < nt) load(warp + kW, id, ppt);
@@ -325,14 +327,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t poff = pg * pitch + lay.kp + 4 * (ing + (g & 1));
   const uint32_t voff = pt * pitch + lay.v + in + g * ps;
   const int jg = 16 * (g >> 1) + (g & 1);
-  // Tile k is phase n = k / kStages of its stage's barrier.  A wait names only
-  // the parity of a phase, and phase n - 1 is another warp's tile, perhaps not
-  // landed yet: so first the stage has to be armed for phase n, which the warp
-  // that loads into it writes down.
+  // Phase k / kStages - 1 of tile k's stage is another warp's tile, perhaps not
+  // landed yet: so the stage's word first (ring_armed).
   auto landed = [&](int k) -> bool {
-    const int s = k % kStages, n = k / kStages;
-    bool done = n == 0 || bounded_armed(gen + s, n, a.t);
-    done = done && bounded_wait(bar + 8 * s, n & 1, a.t);
+    bool done = bounded_armed(armed, k, a.t);
+    done = done && bounded_wait(bar + 8 * (k % kStages), k / kStages & 1, a.t);
     return __all_sync(0xffffffffu, done);
   };
   bool ok = true;

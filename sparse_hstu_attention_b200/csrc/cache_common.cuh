@@ -155,6 +155,24 @@ __host__ __device__ __forceinline__ CacheFull cache_full(int r0, int r1, int h, 
   return f;
 }
 
+// A block's key tiles k = 0, 1, ... go round a ring of `stages` stages, tile k as
+// phase k / stages of its stage's barrier.  A wait on that barrier names only the
+// phase's parity, and so also passes while the phase before is still in flight; on a
+// barrier that nothing was loaded to yet, the wait for phase 1 does.  So a word per
+// stage says which phase it is armed for, none to begin with, and a warp waits for
+// phase 1 and up only once that is the phase.  ring_clear comes before a barrier of
+// the block that all its loads and waits come after.
+__host__ __device__ __forceinline__ void ring_clear(volatile int* armed, int stages) {
+  for (int s = 0; s < stages; ++s) armed[s] = -1;
+}
+__host__ __device__ __forceinline__ void ring_arm(volatile int* armed, int k, int stages) {
+  armed[k % stages] = k / stages;
+}
+__host__ __device__ __forceinline__ bool ring_armed(const volatile int* armed, int k,
+                                                    int stages) {
+  return k < stages || armed[k % stages] == k / stages;
+}
+
 // A kernel launched by launch_early starts before the one ahead of it in the
 // stream has ended, and waits for that here.
 __device__ __forceinline__ void wait_for_the_last_kernel() {

@@ -224,3 +224,15 @@ def test_more_blocks_than_a_grid_are_refused(lib, max_new, total):
     assert lib.hstu_cache_attend(t, p, FAKE, 1 << 60, None) == _abi.ERR_UNSUPPORTED
     assert lib.hstu_cache_attend(_tables(B=(1 << 30) + 1), p, FAKE, 1 << 60,
                                  None) == _abi.ERR_UNSUPPORTED
+
+
+def test_the_ring_of_key_tiles_never_runs_ahead(tmp_path):
+    """No order of the warps and copies lets a warp take a stage before its tile, whatever
+    shared memory held; with the stages' words left as they were, some do."""
+    exe = str(tmp_path / "cache_ring_check")
+    subprocess.check_call(["/usr/local/cuda/bin/nvcc", "-std=c++17", "-O2",
+                           "-Wno-deprecated-gpu-targets", "-x", "cu",
+                           os.path.join(ROOT, "tests", "cache_ring_check.cu"), "-o", exe])
+    for args in (["3000"], ["3000", "keep"]):
+        r = subprocess.run([exe, *args], capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and r.stdout.startswith("OK"), r.stdout + r.stderr

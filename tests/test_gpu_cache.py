@@ -725,3 +725,21 @@ def test_sizes_beyond_their_fields_are_refused():
                 dict(page_size=48)):
         with pytest.raises(ValueError):
             cache.CacheTables(t.buf, **{**dict(B=1, max_pages=2, num_pages=3, page_size=16), **bad})
+
+
+def test_long_reads_repeat_themselves():
+    """Blocks that go round their ring of key tiles several times, behind others that
+    leave other phases in shared memory: every call gives the same bits."""
+    H, d, ps = 4, 64, 32
+    t, pages, _ = filled([2000, 1500, 900], H, d, ps, 29)
+    runs = []
+    for rows in (1, 5):
+        q = silu_rows(3 * rows, H, d, rows)[0].to(DEV)
+        for K1 in (1 << 20, 700):
+            args = (q, None, None, offs_of([rows] * 3), None, pages, t)
+            kw = dict(contextual_len=0, K1=K1, K2=0, alpha=0.2, N=50.0, max_new=rows)
+            runs.append((args, kw, cache.attend(*args, **kw)))
+    for _ in range(50):
+        for args, kw, want in runs:
+            assert torch.equal(cache.attend(*args, **kw), want)
+    assert cache.get_error(t) == 0
