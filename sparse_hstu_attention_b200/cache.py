@@ -19,9 +19,10 @@ slot, of any number of rows (none for a slot with nothing new).  There is no
 gradient: the outputs are new tensors outside autograd.
 
 Calls run on the tensors' own device, on its current stream unless `stream` is
-given, and allocate only their outputs (and plan its scratch).  They can be
-captured into a CUDA graph and replayed with other lengths, counts and offsets
-in the same tensors: nothing about them is read on the host.
+given, and allocate only their outputs (and plan and attend their scratch), from
+the memory of the stream they run on.  They can be captured into a CUDA graph and
+replayed with other lengths, counts and offsets in the same tensors: nothing about
+them is read on the host.
 """
 from __future__ import annotations
 
@@ -199,24 +200,29 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, dev, stream):
     if workspace is None:
         if need == 0:
             return None
-        workspace = _made(torch.empty(need, dtype=torch.uint8, device=dev), stream)
+        workspace = _new(need, torch.uint8, dev, stream, out=False)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or \
             not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
     return workspace
 
 
-def _made(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor that a call allocates: kept from reuse until `stream`, if one is
-    given, is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
+def _new(size, dtype, device, stream, out: bool = True) -> torch.Tensor:
+    """A tensor that a call allocates: from the memory of the stream that writes it, since
+    what another stream has just released may still be in use there.  An output is then
+    kept from reuse until the current stream, where the caller goes on, is done too."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(size, dtype=dtype, device=device)
+    if out:
+        t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
 def _slots_out(slots, total_tokens, dev, stream):
     if slots is None:
-        return _made(torch.empty(total_tokens, dtype=torch.int64, device=dev), stream)
+        return _new(total_tokens, torch.int64, dev, stream)
     _slots(slots, dev)
     if slots.numel() != total_tokens:
         raise ValueError(f"slots must have {total_tokens} elements")
@@ -272,11 +278,11 @@ def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
     T = slots.numel()
     k_rs = v_rs = H * d
     if k is None:
-        k = _made(torch.empty(T, H, d, dtype=torch.bfloat16, device=dev), stream)
+        k = _new((T, H, d), torch.bfloat16, dev, stream)
     else:
         k_rs = _rows(k, "k", T, H, d, dev)
     if v is None:
-        v = _made(torch.empty(T, H, d, dtype=torch.bfloat16, device=dev), stream)
+        v = _new((T, H, d), torch.bfloat16, dev, stream)
     else:
         v_rs = _rows(v, "v", T, H, d, dev)
     r = _pack(_abi.CACHE_ROWS, H, d, T, slots.data_ptr(), pages.data_ptr(), stride, k.data_ptr(),
@@ -308,7 +314,7 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
         k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
     o_rs = H * d
     if out is None:
-        out = _made(torch.empty_like(q, memory_format=torch.contiguous_format), stream)
+        out = _new((T, H, d), torch.bfloat16, dev, stream)
     else:
         o_rs = _rows(out, "out", T, H, d, dev)
     p = _pack(_abi.CACHE_ATTEND, H, d, T, T if max_new is None else int(max_new),

@@ -236,3 +236,38 @@ def test_the_ring_of_key_tiles_never_runs_ahead(tmp_path):
     for args in (["3000"], ["3000", "keep"]):
         r = subprocess.run([exe, *args], capture_output=True, text=True, timeout=300)
         assert r.returncode == 0 and r.stdout.startswith("OK"), r.stdout + r.stderr
+
+
+def test_what_a_call_allocates_comes_from_its_stream(monkeypatch):
+    """With a stream given, outputs and scratch are allocated with that stream current,
+    and only outputs are kept for the caller's; without one, nothing is switched."""
+    now, made, kept = ["caller's"], [], []
+
+    class Current:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            now.append(self.stream)
+
+        def __exit__(self, *_):
+            now.pop()
+
+    empty = torch.empty
+
+    def recorded_empty(*a, **kw):
+        made.append(now[-1])
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch.cuda, "stream", Current)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: now[-1])
+    monkeypatch.setattr(torch, "empty", recorded_empty)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: kept.append((t.dtype, s)),
+                        raising=False)
+    cpu = torch.device("cpu")
+    for stream, where in ((None, "caller's"), ("given", "given")):
+        made.clear(), kept.clear()
+        assert cache._slots_out(None, 5, cpu, stream).shape == (5,)
+        assert cache._workspace(None, 256, cpu, stream).dtype == torch.uint8
+        assert made == [where] * 2
+        assert kept == ([] if stream is None else [(torch.int64, "caller's")])

@@ -743,3 +743,44 @@ def test_long_reads_repeat_themselves():
         for args, kw, want in runs:
             assert torch.equal(cache.attend(*args, **kw), want)
     assert cache.get_error(t) == 0
+
+
+def test_a_given_stream_leaves_released_memory_alone():
+    """Memory released while the current stream still has work on it is not what a call
+    on another stream writes, and an output released right behind its use is not written
+    again before that use."""
+    H, d, ps, rows = 2, 64, 32, 70
+    t, pages, _ = filled([3000, 20], H, d, ps, 30)
+    q, k, v = (x.to(DEV) for x in silu_rows(2 * rows, H, d, 1))
+    offs, nts = offs_of([rows, rows]), dev32([rows, rows - 1])
+    last = offs_of([20, 20])
+    slots = cache.slot_map(t, last, total_tokens=40)
+    kw = dict(contextual_len=0, K1=1 << 20, K2=0, alpha=0.2, N=50.0, max_new=rows)
+    calls = [lambda s: cache.attend(q, k, v, offs, nts, pages, t, stream=s, **kw),
+             lambda s: cache.read(slots, pages, t, stream=s)[1],
+             lambda s: cache.slot_map(t, last, total_tokens=40, stream=s)]
+    want = [f(None) for f in calls]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for f, w in zip(calls, want):
+        for _ in range(3):
+            # as many bytes as the call's output, still to be read here
+            held = torch.full_like(w, 7)
+            seen = torch.empty_like(held)
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20_000_000)  # some 10 ms
+            seen.copy_(held)
+            del held
+            got = f(s)
+            s.synchronize()
+            assert torch.equal(got, w)
+            assert bool((seen == 7).all())
+            # the other way: an output still to be read here, its memory given back
+            torch.cuda._sleep(20_000_000)
+            seen.copy_(got)
+            del got
+            with torch.cuda.stream(s):
+                after = torch.full_like(w, 3)
+            torch.cuda.synchronize()
+            assert torch.equal(seen, w) and bool((after == 3).all())
+    assert cache.get_error(t) == 0
