@@ -153,8 +153,9 @@ int hstu_cache_read(const hstu_cache_tables* t, const hstu_cache_rows* r, hstu_s
  * finite while |alpha| max|q| and the steps s are below 2^100 and the sums are.
  *
  * A sequence whose offsets, targets, length or page ids are out of range, or
- * which has more than max_new rows, sets status (HSTU_SLA_ERR_BAD_INPUT); out's
- * rows are then unspecified.  2^29 blocks (B H times max_new in 128s, or in 8s for
+ * which has more than max_new rows, sets status (HSTU_SLA_ERR_BAD_INPUT), also in a
+ * call with max_new or total_tokens 0; out's rows are then unspecified.  (Page ids are
+ * checked where they are read.)  2^29 blocks (B H times max_new in 128s, or in 8s for
  * few rows) are the most there can be: beyond, HSTU_SLA_ERR_UNSUPPORTED. */
 typedef struct {
   int32_t H;

@@ -570,6 +570,14 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// A thread a sequence: the checks of a call that has no rows to compute.
+__global__ void __launch_bounds__(kThreads)
+    cache_check_kernel(const __grid_constant__ CacheAttnArgs a) {
+  const int b = (int)(blockIdx.x * kThreads + threadIdx.x);
+  CacheSeq sq;
+  if (b < a.t.B) cache_seq(a, b, &sq);
+}
+
 // Blocks a unit.  Two blocks fit an SM.  A unit is split until the GPU is full
 // once, and further, down to 8 tiles a warp, until it is full eight times, so
 // that the last blocks to finish cost little of the whole (64 sequences x 4
@@ -643,7 +651,11 @@ size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d) {
 }
 
 cudaError_t launch_cache_attend(const CacheAttnArgs& a, int d, void* ws, cudaStream_t st) {
-  if (a.T == 0 || a.max_new == 0) return cudaSuccess;
+  if (a.max_new == 0) {  // or no rows at all
+    const unsigned blocks = (unsigned)(((int64_t)a.t.B + kThreads - 1) / kThreads);
+    cache_check_kernel<<<blocks, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
   if (!few_rows(a)) return launch_cache_tc(a, d, ws, st);
   float* parts = static_cast<float*>(ws);
   if (d == 32) return launch_step<32>(a, parts, st);

@@ -784,3 +784,40 @@ def test_a_given_stream_leaves_released_memory_alone():
             torch.cuda.synchronize()
             assert torch.equal(seen, w) and bool((after == 3).all())
     assert cache.get_error(t) == 0
+
+
+@pytest.mark.parametrize("total,most,offs,nts,length,code", [
+    (6, 0, [0, 3, 6], [0, 0], 40, _abi.ERR_BAD_INPUT),     # rows where none are announced
+    (6, 0, [0, 0, 1], [0, 1], 40, _abi.ERR_BAD_INPUT),
+    (6, 0, [0, 0, 0], [0, 0], 40, 0),
+    (0, None, [0, 0, 2], [0, 0], 40, _abi.ERR_BAD_INPUT),  # offsets beyond no rows
+    (0, None, [0, 1, 0], [0, 0], 40, _abi.ERR_BAD_INPUT),
+    (0, None, [0, 0, 0], [0, 1], 40, _abi.ERR_BAD_INPUT),
+    (0, None, [0, 0, 0], [0, 0], -1, _abi.ERR_BAD_INPUT),
+    (0, 5, [0, 0, 0], [0, 0], 1 << 20, _abi.ERR_BAD_INPUT),
+    (0, 5, [0, 0, 0], [0, 0], 40, 0)])
+def test_attend_without_rows_still_checks(total, most, offs, nts, length, code):
+    H, d, ps = 2, 32, 16
+    t, pages, _ = filled([60, 40], H, d, ps, 31)
+    t.lengths[1] = length
+    q, k, v = (x.to(DEV) for x in silu_rows(total, H, d, 0))
+    out = torch.full_like(q, 5.0)
+    cache.attend(q, k, v, dev32(offs), dev32(nts), pages, t, contextual_len=0, K1=8, K2=0,
+                 alpha=0.1, N=9.0, max_new=most, out=out)
+    assert cache.get_error(t) == code and bool((out == 5).all())
+
+
+def test_attend_without_rows_checks_every_sequence():
+    B = 700
+    t = cache.allocate_tables(B, 1, 1, page_size=16, device=DEV)
+    pages = cache.allocate_pages(1, 1, 32, 16, DEV)
+    q = torch.empty((0, 1, 32), dtype=torch.bfloat16, device=DEV)
+    offs = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    for bad in (None, 0, 255, 256, 699):
+        t.status.zero_()
+        t.lengths.zero_()
+        if bad is not None:
+            t.lengths[bad] = -1
+        cache.attend(q, None, None, offs, None, pages, t, contextual_len=0, K1=8, K2=0,
+                     alpha=0.1, N=9.0)
+        assert cache.get_error(t) == (0 if bad is None else _abi.ERR_BAD_INPUT)
