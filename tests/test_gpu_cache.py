@@ -821,3 +821,33 @@ def test_attend_without_rows_checks_every_sequence():
         cache.attend(q, None, None, offs, None, pages, t, contextual_len=0, K1=8, K2=0,
                      alpha=0.1, N=9.0)
         assert cache.get_error(t) == (0 if bad is None else _abi.ERR_BAD_INPUT)
+
+
+def test_a_set_status_stops_every_call():
+    """While the last plan has failed, append, read and either attention kernel, split or
+    not, leave everything as it was; slot_map gives no slot; the next plan frees them."""
+    H, d, ps = 2, 64, 32
+    for lengths in ([3000, 2900], [70, 40]):
+        t, pages, _ = filled(lengths, H, d, ps, 32)
+        cache.plan(t, offs_of([10 ** 4, 0]), total_tokens=10 ** 4)
+        assert cache.get_error(t) != 0
+        code, before = cache.get_error(t), (t.buf.clone(), pages.clone())
+        slots = cache.slot_map(t, offs_of([5, 5]), total_tokens=10)
+        assert bool((slots == -1).all())
+        slots = torch.arange(10, device=DEV)
+        k, v = (x.to(DEV) for x in silu_rows(10, H, d, 1)[1:])
+        cache.append(k, v, slots, pages, t)
+        back = [torch.full_like(k, 5.0) for _ in range(2)]
+        cache.read(slots, pages, t, k=back[0], v=back[1])
+        assert all(bool((x == 5).all()) for x in back)
+        for rows, most in ((1, 1), (5, 5), (70, 70), (0, 0)):
+            for cand in (None, dev32([rows, rows])):
+                q, k, v = (x.to(DEV) for x in silu_rows(2 * rows, H, d, 2))
+                out = torch.full_like(q, 5.0)
+                cache.attend(q, k, v, offs_of([rows, rows]), cand, pages, t, contextual_len=0,
+                             K1=1 << 20, K2=0, alpha=0.1, N=9.0, max_new=most, out=out)
+                assert bool((out == 5).all())
+        assert cache.get_error(t) == code
+        assert torch.equal(t.buf, before[0]) and torch.equal(pages, before[1])
+        cache.plan(t, offs_of([1, 0]), total_tokens=1)
+        assert cache.get_error(t) == 0
