@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 7) cache_append_kernel(CacheRowArgs 
   constexpr int LPR = D / 8, RPI = kThreads / LPR;  // lanes a row, rows an iteration
   using G = Groups<TT>;
   __shared__ G g;
-  __shared__ uint8_t sv[D / 2 * G::kPitch];
+  __shared__ __align__(16) uint8_t sv[D / 2 * G::kPitch];  // (words of it are moved)
   const int64_t t0 = (int64_t)blockIdx.x * TT;
   const int h = blockIdx.y, ps = a.t.ps;
   const PageLayout<D> lay(ps);
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 7) cache_read_kernel(CacheRowArgs a)
   constexpr int LPR = D / 8, RPI = kThreads / LPR;
   using G = Groups<TT>;
   __shared__ G g;
-  __shared__ uint8_t sv[D / 2 * G::kPitch];
+  __shared__ __align__(16) uint8_t sv[D / 2 * G::kPitch];  // (words of it are moved)
   const int64_t t0 = (int64_t)blockIdx.x * TT;
   const int h = blockIdx.y, ps = a.t.ps;
   const PageLayout<D> lay(ps);

@@ -3,6 +3,7 @@ compare with, the masks and key tiles, and the refusals of the C ABI and the
 binding."""
 import ctypes
 import os
+import re
 import subprocess
 
 import numpy as np
@@ -271,3 +272,17 @@ def test_what_a_call_allocates_comes_from_its_stream(monkeypatch):
         assert cache._workspace(None, 256, cpu, stream).dtype == torch.uint8
         assert made == [where] * 2
         assert kept == ([] if stream is None else [(torch.int64, "caller's")])
+
+
+def test_bytes_in_shared_memory_state_their_alignment():
+    """A byte array in shared memory has an alignment of one unless it says otherwise,
+    and the kernels read theirs as words.  (Those of a launch's own size are aligned by
+    the kernel, from their address.)"""
+    found = 0
+    for name in sorted(os.listdir(os.path.join(_abi.PKG, "csrc"))):
+        text = open(os.path.join(_abi.PKG, "csrc", name)).read()
+        for m in re.finditer(r"(extern )?__shared__ ([^;]*\b(?:u?int8_t|(?:unsigned )?char) [^;]*);",
+                             text):
+            found += 1
+            assert m[1] or re.match(r"__align__\((4|8|16|128)\) ", m[2]), (name, m[0])
+    assert found > 5
