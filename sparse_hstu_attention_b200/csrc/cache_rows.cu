@@ -6,8 +6,9 @@
 // by adding 1.5 2^23 and the packing of 8 codes by multiply-adds with powers of
 // 16 (mod 2^32; what the added constant leaves is taken off at the end).  Even
 // lanes divide for K and odd ones for V.  Read: bf16(m + s code) by one bf16
-// multiply-add, which rounds once; since s code has at most 12 bits, that is
-// also what fp32 rounded to bf16 gives.
+// multiply-add, which rounds once.  (Rounding to fp32 on the way is not the same:
+// s code may lie midway between two bf16 numbers, where a small m decides and fp32
+// has lost it.)
 //
 // V codes lie dim pair by dim pair, so one row's bytes are page_size apart.
 // Rows of one sequence come in runs of consecutive slots: a run's part in one

@@ -30,6 +30,13 @@ def values(x):
     return m[..., None] + s[..., None] * c
 
 
+def bf16_once(x):
+    """float64 rounded to bf16 once, ties to even (torch goes through fp32)."""
+    x = x.double().numpy()
+    e = np.maximum(np.frexp(x)[1], -125)
+    return torch.from_numpy(np.ldexp(np.rint(np.ldexp(x, 8 - e)), e - 8))
+
+
 def offsets(H, d, ps):
     """Byte offsets within a page of (head, token, dim): K byte, K shift, V byte,
     V shift; and of the (step, minimum) pairs of K and V."""

@@ -68,6 +68,20 @@ def test_quantisation_error_is_half_a_step():
     assert torch.isnan(ref.values(odd)).all()
 
 
+def test_bf16_once_rounds_to_the_nearest():
+    """On fp32 numbers it is torch's rounding (subnormal ones too); on numbers next to a
+    midpoint it goes to the side they are on."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randint(-2 ** 31, 2 ** 31, (20000,), generator=g).int().view(torch.float32)
+    x = x[x.abs() < 3e38]
+    assert torch.equal(ref.bf16_once(x), x.bfloat16().double())
+    assert (x.abs() < 2.0 ** -126).any()
+    mid = 1 + 2.0 ** -8
+    x = torch.tensor([mid, mid + 2.0 ** -40, mid - 2.0 ** -40, -mid - 2.0 ** -40],
+                     dtype=torch.float64)
+    assert ref.bf16_once(x).tolist() == [1, 1 + 2.0 ** -7, 1, -1 - 2.0 ** -7]
+
+
 def _tables(**kw):
     t = _abi.CacheTablesC(4, 8, 32, 64, FAKE, FAKE, FAKE, FAKE, FAKE)
     for k, v in kw.items():

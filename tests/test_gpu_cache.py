@@ -851,3 +851,30 @@ def test_a_set_status_stops_every_call():
         assert torch.equal(t.buf, before[0]) and torch.equal(pages, before[1])
         cache.plan(t, offs_of([1, 0]), total_tokens=1)
         assert cache.get_error(t) == 0
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("ahead", [-40, -30, -26])
+def test_read_rounds_once(d, ahead):
+    """Rows whose s code lies midway between two bf16 numbers (s = 129/2048, codes 3, 6
+    and 12) with a minimum below fp32's resolution of it: bf16(m + s code) rounds once."""
+    H, ps, T = 2, 16, 40
+    g = torch.Generator().manual_seed(d)
+    k = torch.rand((T, H, d), generator=g) * (242 / 256)
+    k[..., 1] = 242 / 256
+    v = k.flip(-1).clone()
+    low = torch.where(torch.arange(T) % 2 == 0, -1.0, 1.0) * 2.0 ** ahead
+    k[..., 0], v[..., 5] = low[:, None], low[:, None]
+    k, v = k.bfloat16(), v.bfloat16()
+    t = cache.allocate_tables(1, 1, 4, page_size=ps, device=DEV)
+    pages = cache.allocate_pages(4, H, d, ps, DEV)
+    slots = torch.randperm(4 * ps, generator=g)[:T].to(DEV)
+    cache.append(k.to(DEV), v.to(DEV), slots, pages, t)
+    for x, got in zip((k, v), cache.read(slots, pages, t)):
+        code, s, m = ref.quantise(x)
+        assert bool((s == 129 / 2048).all()) and torch.equal(m, low[:, None].expand(T, H).double())
+        exact = m[..., None] + s[..., None] * code  # (fits 53 bits)
+        want = ref.bf16_once(exact)
+        assert bool((want != exact.float().bfloat16().double()).any())
+        assert torch.equal(got.cpu().double(), want)
+    assert cache.get_error(t) == 0
