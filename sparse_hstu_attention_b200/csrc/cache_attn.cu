@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kThreads)
 // heads of 8K-16K tokens, d = 128, one row: 88 us unsplit, 81 in 4, 88 in 8;
 // 10-tile windows of the same batch: 9 us unsplit, 15 in 2).
 int step_splits(int64_t units, int64_t tiles) {
-  const int64_t slots = 2 * 148;
+  const int64_t slots = 2 * kSMs;
   int64_t fill = (slots + units - 1) / units;
   fill = fill < tiles / kW ? fill : tiles / kW;
   int64_t even = tiles / (8 * kW);
@@ -641,7 +641,7 @@ cudaError_t launch_step(const CacheAttnArgs& a, float* parts, cudaStream_t st) {
 bool few_rows(const CacheAttnArgs& a) {
   const int64_t units = cache_units(a, kRows);
   return a.max_new <= 16 ||
-         (units <= 2 * 148 && a.max_new <= (most_keys(a) <= 4096 ? 64 : 32));
+         (units <= 2 * kSMs && a.max_new <= (most_keys(a) <= 4096 ? 64 : 32));
 }
 
 size_t cache_attend_ws_bytes(const CacheAttnArgs& a, int d) {

@@ -782,7 +782,7 @@ TcPlan tc_plan(const CacheAttnArgs& a) {
   p.units = cache_units(a, kBM);
   const int64_t w = (int64_t)a.K1 + a.K2e + kBM, c = (int64_t)a.t.M * a.t.ps;
   const int64_t tiles = (w < c ? w : c) / kBN + 2;
-  const int64_t slots = 2 * 148, n = p.units > 0 ? p.units : 1;
+  const int64_t slots = 2 * kSMs, n = p.units > 0 ? p.units : 1;
   int64_t fill = slots / n;
   fill = fill < tiles / 2 ? fill : tiles / 2;
   int64_t even = (slots * 3 / 2 + n - 1) / n;

@@ -25,6 +25,10 @@ __device__ __forceinline__ void cache_fail(const CacheTab& t, int code) {
   atomicCAS(t.status, 0, code);
 }
 
+// SMs of a B200; the launch rules count blocks by it.  (Another number would make a
+// rule's choice less apt, not wrong.)
+constexpr int kSMs = 148;
+
 // Byte offsets inside one head's block of a page.
 template <int D>
 struct PageLayout {

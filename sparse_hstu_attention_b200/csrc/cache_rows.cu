@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 7) cache_read_kernel(CacheRowArgs a)
 // with them takes tiles of 16.
 template <int D>
 cudaError_t launch_rows(const CacheRowArgs& a, bool append, cudaStream_t st) {
-  const bool big = (a.T + 127) / 128 * a.H >= 148;
+  const bool big = (a.T + 127) / 128 * a.H >= kSMs;
   const dim3 grid((unsigned)((a.T + (big ? 127 : 15)) / (big ? 128 : 16)), (unsigned)a.H);
   if (append) {
     if (big) cache_append_kernel<D, 128><<<grid, kThreads, 0, st>>>(a);
