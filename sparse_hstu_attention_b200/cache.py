@@ -200,21 +200,21 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, dev, stream):
     if workspace is None:
         if need == 0:
             return None
-        workspace = _new(need, torch.uint8, dev, stream, out=False)
+        workspace = _new(torch.uint8, dev, stream, need, out=False)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or \
             not workspace.is_contiguous() or workspace.numel() < need:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of {need} bytes on {dev}")
     return workspace
 
 
-def _new(size, dtype, device, stream, out: bool = True) -> torch.Tensor:
+def _new(dtype, device, stream, *size, out: bool = True) -> torch.Tensor:
     """A tensor that a call allocates: from the memory of the stream that writes it, since
     what another stream has just released may still be in use there.  An output is then
     kept from reuse until the current stream, where the caller goes on, is done too."""
-    if stream is None:
-        return torch.empty(size, dtype=dtype, device=device)
+    if stream is None:  # (the sizes one by one: a tuple of them costs 1 us)
+        return torch.empty(*size, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        t = torch.empty(size, dtype=dtype, device=device)
+        t = torch.empty(*size, dtype=dtype, device=device)
     if out:
         t.record_stream(torch.cuda.current_stream(device))
     return t
@@ -222,7 +222,7 @@ def _new(size, dtype, device, stream, out: bool = True) -> torch.Tensor:
 
 def _slots_out(slots, total_tokens, dev, stream):
     if slots is None:
-        return _new(total_tokens, torch.int64, dev, stream)
+        return _new(torch.int64, dev, stream, total_tokens)
     _slots(slots, dev)
     if slots.numel() != total_tokens:
         raise ValueError(f"slots must have {total_tokens} elements")
@@ -278,11 +278,11 @@ def read(slots: torch.Tensor, pages: torch.Tensor, tables: CacheTables, *,
     T = slots.numel()
     k_rs = v_rs = H * d
     if k is None:
-        k = _new((T, H, d), torch.bfloat16, dev, stream)
+        k = _new(torch.bfloat16, dev, stream, T, H, d)
     else:
         k_rs = _rows(k, "k", T, H, d, dev)
     if v is None:
-        v = _new((T, H, d), torch.bfloat16, dev, stream)
+        v = _new(torch.bfloat16, dev, stream, T, H, d)
     else:
         v_rs = _rows(v, "v", T, H, d, dev)
     r = _pack(_abi.CACHE_ROWS, H, d, T, slots.data_ptr(), pages.data_ptr(), stride, k.data_ptr(),
@@ -314,7 +314,7 @@ def attend(q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor]
         k_ptr, v_ptr = k.data_ptr(), v.data_ptr()
     o_rs = H * d
     if out is None:
-        out = _new((T, H, d), torch.bfloat16, dev, stream)
+        out = _new(torch.bfloat16, dev, stream, T, H, d)
     else:
         o_rs = _rows(out, "out", T, H, d, dev)
     p = _pack(_abi.CACHE_ATTEND, H, d, T, T if max_new is None else int(max_new),
