@@ -151,6 +151,15 @@ int hstu_cache_read(const hstu_cache_tables* t, const hstu_cache_rows* r, hstu_s
  * A row of q that holds a NaN or an infinity gives a NaN row (if it sees a key).
  * Sums are held in fp32 and scaled inside by up to 2^24: finite inputs stay
  * finite while |alpha| max|q| and the steps s are below 2^100 and the sums are.
+ * Fewer bits than fp32 have, as in hstu_sla_fwd: SiLU over the cached keys, which
+ * takes tanh from the GPU's instruction (relative error about 2^-11), and its product
+ * with a key's step of V, an operand of the second matrix product: f16 scaled by a
+ * power of two per row in the kernel of few rows (off by up to 2^-11 of itself, and by
+ * 2^-29 of the largest for what is more than 2^18 below that), bf16 in the one of many
+ * rows (up to 2^-8).  The result is rounded to bf16 once, at the end.
+ *
+ * There is no relative attention bias here (hstu_sla_fwd's rab_pos, rab_time): a model
+ * that has one is scored from the whole history.
  *
  * A sequence whose offsets, targets, length or page ids are out of range, or
  * which has more than max_new rows, sets status (HSTU_SLA_ERR_BAD_INPUT), also in a
@@ -161,7 +170,9 @@ typedef struct {
   int32_t H;
   int32_t d;                   /* 32, 64 or 128 */
   int64_t total_tokens;        /* rows of q, k, v, out; >= seq_offsets[B] */
-  int32_t max_new;             /* >= every sequence's rows (device-checked) */
+  int32_t max_new;             /* >= every sequence's rows (device-checked); it and the
+                                  tables' max_pages choose the kernel, the splits and the
+                                  workspace, so a tight bound is a quicker call */
   const int32_t* seq_offsets;  /* device [B + 1] */
   const int32_t* num_targets;  /* device [B] or NULL */
   int32_t contextual_len, K1, K2;

@@ -17,8 +17,10 @@
 // events of many users) moves single bytes.
 //
 // Bound: bytes (append reads 4 d and writes d + 8 per token and head), with
-// issue slots close behind: 100k rows of 4 x 128 stored and read back in 113 us,
-// 4.6 TB/s; unrolled loops with fewer blocks an SM take 116 to 130.
+// issue slots close behind: 100k rows of 4 x 128 stored in 63 us (4.1 TB/s) and read
+// back in 53 (4.9 TB/s); unrolled loops with fewer blocks an SM take 116 to 130 for both.
+// (At d = 32 the 32 registers of 7 blocks an SM leave the append of 128-row tiles 60
+// bytes a thread in local memory.)
 #include "cache_common.cuh"
 #include "sm100.cuh"
 
@@ -301,7 +303,10 @@ __global__ void __launch_bounds__(kThreads, 7) cache_read_kernel(CacheRowArgs a)
 }
 
 // Tiles of 128 rows gather whole groups; a batch too small to fill the GPU
-// with them takes tiles of 16.
+// with them takes tiles of 16.  Measured, 16 rows / 128, append and read, us: 4 heads of
+// 128, 1024 rows 3.4 / 8.0 and 3.1 / 5.4, 4096 rows 6.1 / 8.1 and 5.5 / 5.5, 8192 rows 8.7 /
+// 9.4 and 8.8 / 6.5, 32768 rows 25.6 / 22.4 and 27.9 / 16.3; 1 head of 32, 8192 rows 3.6 /
+// 3.7 and 3.5 / 3.1, 32768 rows 7.0 / 4.6 and 7.0 / 3.6.
 template <int D>
 cudaError_t launch_rows(const CacheRowArgs& a, bool append, cudaStream_t st) {
   const bool big = (a.T + 127) / 128 * a.H >= kSMs;
